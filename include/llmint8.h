@@ -319,6 +319,82 @@ LLMINT8_API int llmint8_smoothquant_matmul_debug(const void* X, int64_t T, int64
                                                  void* stream);
 
 /*
+ * Products of int8 codes with token and channel scales, dense and grouped by
+ * expert.  The pages quantise one scale per output channel of W ('LLM
+ * quantization, part 2' §2.1) and dequantise as r' = s * q ('三、模型量化' Q2);
+ * these entries take codes that are already there (one quantised input serves
+ * several projections, or several experts) and serve inference only.
+ * None takes a workspace, so calls on several streams, or in several captured
+ * graphs, do not meet.  K <= 65536.
+ */
+typedef enum { LLMINT8_F16 = 0, LLMINT8_BF16 = 1, LLMINT8_F32 = 2 } llmint8_dtype;
+
+/*
+ * Row quantisation of X [T][K] (`dtype`): scale s = max_k |X[t,k]| / 127, codes
+ * rint_even(X[t,k] / s) (binary32; 0 when s == 0).  A row that holds a NaN or
+ * an infinity gets s = NaN and codes 0: its products are NaN, no other row's.
+ *   positions NULL: Xq int8 [T][K], xscale float [T]; S == T.
+ *   positions int32 [T][copies]: row t goes to every row positions[t][j] >= 0
+ *     of Xq [S][K], xscale [S] (a mixture of experts' order, as
+ *     llmint8_expert_positions gives it); -1 is skipped, rows that no position
+ *     names are left as they were.  Positions must be distinct: which of two
+ *     rows with one position stays is not defined.  A position below -1 or
+ *     from S on is skipped and recorded; llmint8_sync_status then reports
+ *     LLMINT8_ERR_INVALID_ARG.
+ */
+LLMINT8_API int llmint8_quantize_rows(const void* X, int dtype, int64_t T, int64_t K, const int32_t* positions,
+                                      int64_t copies, int64_t S, int8_t* Xq, float* xscale, void* stream);
+
+/*
+ * z[t,n] = (sum_k Xq[t,k] Wq[n,k]) xscale[t] Wscale[n] (+ bias[n]): the sum exact
+ * in int32, the rest binary32, Y rounded once to `dtype`.
+ *   Xq int8 [T][K], xscale float [T], Wq int8 [N][K], Wscale float [N],
+ *   bias float [N] or NULL.
+ *   gated 0: Y [T][N] = z.
+ *   gated 1: N = 2F with F % 16 == 0 (gate rows of Wq first, then the F value
+ *     rows); Y [T][F] = silu(z[:, :F]) * z[:, F:], silu(g) = g / (1 + exp(-g)).
+ */
+LLMINT8_API int llmint8_scaled_matmul(const int8_t* Xq, const float* xscale, int64_t T, int64_t K, const int8_t* Wq,
+                                      const float* Wscale, const float* bias, int64_t N, int gated, void* Y,
+                                      int dtype, void* stream);
+
+/*
+ * The same for rows grouped by expert: rows offsets[e] .. offsets[e+1] - 1 of
+ * Xq [S][K] meet Wq[e], Wscale[e], bias[e] of Wq int8 [E][N][K], Wscale float
+ * [E][N], bias float [E][N] or NULL.  offsets int32 [E+1] on the device, not
+ * decreasing, within [0, S]; a group may be empty.  Rows of Y outside
+ * [offsets[0], offsets[E]) are left as they were.  1 <= E <= 1024.  Offsets
+ * that decrease or leave [0, S] are clamped and recorded; llmint8_sync_status
+ * then reports LLMINT8_ERR_INVALID_ARG.
+ */
+LLMINT8_API int llmint8_grouped_matmul(const int8_t* Xq, const float* xscale, int64_t S, int64_t K,
+                                       const int32_t* offsets, int64_t E, const int8_t* Wq, const float* Wscale,
+                                       const float* bias, int64_t N, int gated, void* Y, int dtype, void* stream);
+
+/*
+ * The order of a router's choices by expert, stable in the order of ids [T][k]
+ * (id_bytes 4 or 8: signed integers):
+ *   offsets int32 [E+1]: expert e's rows begin at offsets[e]; offsets[E] = rows
+ *     in all.
+ *   positions int32 [T][k]: the row of each choice; -1 where the id is outside
+ *     [0, E) (a padding token, a dropped choice).
+ * 1 <= E <= 1024.  T == 0 writes the offsets (all 0).
+ */
+LLMINT8_API int llmint8_expert_positions(const void* ids, int id_bytes, int64_t T, int64_t k, int64_t E,
+                                         int32_t* positions, int32_t* offsets, void* stream);
+
+/*
+ * out[t] = sum_j weights[t][j] * Y[positions[t][j]] over the positions >= 0,
+ * binary32 in ascending j, rounded once.  Y [S][N] (`y_dtype`), positions int32
+ * [T][k], weights float [T][k], out [T][N] (`out_dtype`).  A token without any
+ * position gets zeros; rows that no position names are not read.  A position
+ * below -1 or from S on counts as none and is recorded, as above.
+ */
+LLMINT8_API int llmint8_expert_combine(const void* Y, int y_dtype, int64_t S, int64_t N, const int32_t* positions,
+                                       const float* weights, int64_t T, int64_t k, void* out, int out_dtype,
+                                       void* stream);
+
+/*
  * llmint8_matmul for decode shapes (T <= 16) without a caller workspace and
  * without allocating anything.  The pages have no counterpart: this entry
  * serves callers that cannot call cudaMalloc, such as a host program that owns
@@ -346,7 +422,8 @@ LLMINT8_API int llmint8_matmul_decode_noalloc(const void* X, int64_t T, int64_t 
  * Waits for `stream`, then reads and clears this device's error word.
  * Returns LLMINT8_ERR_TIMEOUT if a kernel gave up a bounded wait since the
  * last call, LLMINT8_ERR_INVALID_ARG if llmint8_outlier_store_build met a
- * column outside [0, K), LLMINT8_ERR_CUDA if the stream reported an error,
+ * column outside [0, K) or another call a position or an offset outside its
+ * buffer, LLMINT8_ERR_CUDA if the stream reported an error,
  * else OK.
  */
 LLMINT8_API int llmint8_sync_status(void* stream);

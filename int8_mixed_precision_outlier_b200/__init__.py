@@ -13,3 +13,7 @@ from .llmint8 import (  # noqa: F401
     llmint8_smoothquant_matmul, llmint8_fp8_quantize_weight, llmint8_fp8_matmul, llmint8_outlier_store_build,
     llmint8_matmul_stored,
 )
+from .products import (  # noqa: F401
+    MAX_EXPERTS, llmint8_expert_combine, llmint8_expert_positions, llmint8_grouped_matmul, llmint8_quantize_rows,
+    llmint8_scaled_matmul,
+)

@@ -17,9 +17,11 @@
 
 #include "llmint8.h"
 
+#include "expert_kernels.cuh"
 #include "gemm_kernel.cuh"
 #include "gemv_kernel.cuh"
 #include "prep_kernels.cuh"
+#include "product_kernel.cuh"
 #include "sm100.cuh"
 #include "smooth_kernels.cuh"
 
@@ -71,6 +73,24 @@ cudaError_t set_attributes() {
   return e;
 }
 
+// Shared-memory limits of the products with token and channel scales and of
+// the expert positions.
+cudaError_t set_product_attributes() {
+  cudaError_t e = cudaSuccess;
+  auto big = [&](auto kern, int bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  big(product::product_kernel<false, product::kF16>, product::SMEM_BYTES);
+  big(product::product_kernel<false, product::kBF16>, product::SMEM_BYTES);
+  big(product::product_kernel<false, product::kF32>, product::SMEM_BYTES);
+  big(product::product_kernel<true, product::kF16>, product::SMEM_BYTES);
+  big(product::product_kernel<true, product::kBF16>, product::SMEM_BYTES);
+  big(product::product_kernel<true, product::kF32>, product::SMEM_BYTES);
+  big(expert::expert_positions_kernel<int32_t>, expert::pos_smem_bytes(product::MAX_GROUPS));
+  big(expert::expert_positions_kernel<int64_t>, expert::pos_smem_bytes(product::MAX_GROUPS));
+  return e;
+}
+
 int device_info(int* num_sms, int* max_pairs = nullptr) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return LLMINT8_ERR_CUDA;
@@ -88,7 +108,8 @@ int device_info(int* num_sms, int* max_pairs = nullptr) {
       d.status = LLMINT8_ERR_UNSUPPORTED_ARCH;
       return;
     }
-    if (set_attributes<false>() != cudaSuccess || set_attributes<true>() != cudaSuccess) {
+    if (set_attributes<false>() != cudaSuccess || set_attributes<true>() != cudaSuccess ||
+        set_product_attributes() != cudaSuccess) {
       d.status = LLMINT8_ERR_CUDA;
       return;
     }
@@ -168,6 +189,20 @@ bool encode_kblocks_3d(CUtensorMap* map, const void* base, uint64_t rows, uint64
   const cuuint32_t box[3] = {128, box_rows, kpb};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Any tiled map of 8-bit elements with the 128-byte swizzle: dims and boxes
+// innermost first, `strides` in bytes for the dims after the first.
+template <int RANK>
+bool encode_tiled(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[RANK],
+                  const cuuint64_t (&strides)[RANK - 1], const cuuint32_t (&box)[RANK]) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint32_t estr[RANK];
+  for (int i = 0; i < RANK; ++i) estr[i] = 1;
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, RANK, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -592,6 +627,211 @@ int smoothquant_impl(const void* X, int64_t T, int64_t K, const float* s, const 
   });
 }
 
+// ------------------------------------------------------------ products with token and channel scales
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+bool float_dtype(int d) { return d == LLMINT8_F16 || d == LLMINT8_BF16 || d == LLMINT8_F32; }
+
+// How a product is cut into tiles.  Only sizes that the host knows go in: for
+// ragged groups it plans for equally long ones, and the kernel takes whatever
+// lengths the device's offsets give.
+struct ProductPlan {
+  int BT = 0, box = 0, KPB = 0, H = 0, stages = 0;
+  int64_t tiles = 0;  // an upper bound
+};
+
+ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, int num_sms) {
+  ProductPlan best;
+  const int groups = grouped ? std::min(E, S) : 1;
+  const int avg = (S + groups - 1) / groups;
+  const int want = (grouped ? 2 * avg : avg);
+  const int BT = want >= product::MAX_BT ? product::MAX_BT
+                 : want > 64             ? (want + 63) / 64 * 64
+                                         : (want + 15) / 16 * 16;
+  const int box = std::min(BT, 64);
+  const bool ksplit = K % product::BK == 0;
+  const int step = gated ? 32 : 8;
+  double best_cost = -1.0;
+  for (int H = step; H <= product::BM; H += step) {
+    const int nN = (N + H - 1) / H;
+    const int64_t tiles = static_cast<int64_t>(groups) * ((avg + BT - 1) / BT) * nN;
+    const double cost = static_cast<double>((tiles + num_sms - 1) / num_sms) * (H + BT + 32);
+    if (best_cost < 0.0 || cost <= best_cost) {
+      best_cost = cost;
+      best.H = H;
+      best.tiles = (static_cast<int64_t>(S) / BT + groups) * nN;
+    }
+  }
+  best.BT = BT;
+  best.box = box;
+  const int rows = best.H + BT;
+  best.KPB = !ksplit || BT > box ? 1 : rows * product::BK * 16 <= product::RING_BYTES ? 4
+             : rows * product::BK * 8 <= product::RING_BYTES ? 2 : 1;
+  best.KPB = std::min(best.KPB, (K + product::BK - 1) / product::BK);
+  if (best.KPB == 3) best.KPB = 2;
+  best.stages = std::min(product::MAX_STAGES, product::RING_BYTES / (rows * product::BK * best.KPB));
+  return best;
+}
+
+int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const int32_t* offsets, bool grouped,
+                 int64_t E, const int8_t* Wq, const float* sw, const float* bias, int64_t N, int gated, void* Y,
+                 int dtype, void* stream) {
+  if (S < 0 || N < 0 || S > INT32_MAX || N > INT32_MAX || K < 16 || K > kMaxK) return LLMINT8_ERR_INVALID_ARG;
+  if (E < 1 || E > product::MAX_GROUPS || !float_dtype(dtype)) return LLMINT8_ERR_INVALID_ARG;
+  if (gated && N % 32 != 0) return LLMINT8_ERR_INVALID_ARG;
+  if (K % 16 != 0) return LLMINT8_ERR_ALIGNMENT;
+  if (S == 0 || N == 0) return LLMINT8_OK;
+  if (!Xq || !sx || !Wq || !sw || !Y || (grouped && !offsets)) return LLMINT8_ERR_INVALID_ARG;
+  if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || misaligned4(sx) || misaligned4(sw) ||
+      misaligned4(bias) || misaligned4(offsets))
+    return LLMINT8_ERR_ALIGNMENT;
+  int num_sms = 0;
+  const int rc = device_info(&num_sms);
+  if (rc != LLMINT8_OK) return rc;
+  const ProductPlan plan = plan_product(static_cast<int>(S), static_cast<int>(N), static_cast<int>(K),
+                                        static_cast<int>(E), grouped, gated != 0, num_sms);
+  if (plan.tiles > INT32_MAX) return LLMINT8_ERR_INVALID_ARG;
+  product::Params p;
+  p.S = static_cast<int>(S);
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.No = gated ? p.N / 2 : p.N;
+  p.E = static_cast<int>(E);
+  p.offsets = offsets;
+  p.KB = (p.K + product::BK - 1) / product::BK;
+  p.KPB = plan.KPB;
+  p.NU = (p.KB + p.KPB - 1) / p.KPB;
+  p.ksplit = K % product::BK == 0 ? 1 : 0;
+  p.H = plan.H;
+  p.nN = (p.N + p.H - 1) / p.H;
+  p.BT = plan.BT;
+  p.box = plan.box;
+  p.stages = plan.stages;
+  p.sx = sx;
+  p.sw = sw;
+  p.bias = bias;
+  p.Y = Y;
+  p.wait_ns = g_wait_ns.load();
+  // K as [K / 128][128] when it divides, so that one copy brings several
+  // k-blocks of each row, otherwise as one ragged row.
+  const cuuint64_t k0 = p.ksplit ? product::BK : static_cast<cuuint64_t>(K);
+  const cuuint64_t k1 = p.ksplit ? static_cast<cuuint64_t>(K / product::BK) : 1;
+  const cuuint64_t Ku = static_cast<cuuint64_t>(K), Nu = static_cast<cuuint64_t>(N), Eu = static_cast<cuuint64_t>(E);
+  const cuuint32_t kpb = static_cast<cuuint32_t>(p.KPB), H = static_cast<cuuint32_t>(p.H);
+  CUtensorMap tw, tx;
+  const bool ok =
+      (gated ? encode_tiled<5>(&tw, Wq, {k0, 16, 2 * Eu, Nu / 32, k1}, {Ku, Nu / 2 * Ku, 16 * Ku, product::BK},
+                               {product::BK, 16, 2, H / 32, kpb})
+             : encode_tiled<4>(&tw, Wq, {k0, Nu, k1, Eu}, {Ku, product::BK, Nu * Ku}, {product::BK, H, kpb, 1})) &&
+      encode_tiled<3>(&tx, Xq, {k0, static_cast<cuuint64_t>(S), k1}, {Ku, product::BK},
+                      {product::BK, static_cast<cuuint32_t>(p.box), kpb});
+  if (!ok) return LLMINT8_ERR_CUDA;
+  void (*kern)(const CUtensorMap, const CUtensorMap, const product::Params) =
+      gated ? (dtype == LLMINT8_F16    ? product::product_kernel<true, product::kF16>
+               : dtype == LLMINT8_BF16 ? product::product_kernel<true, product::kBF16>
+                                       : product::product_kernel<true, product::kF32>)
+            : (dtype == LLMINT8_F16    ? product::product_kernel<false, product::kF16>
+               : dtype == LLMINT8_BF16 ? product::product_kernel<false, product::kBF16>
+                                       : product::product_kernel<false, product::kF32>);
+  const int grid = static_cast<int>(std::min<int64_t>(num_sms, plan.tiles));
+  const cudaError_t e = launch(kern, dim3(grid), dim3(product::THREADS), product::SMEM_BYTES,
+                               static_cast<cudaStream_t>(stream), true, tw, tx, p);
+  return e == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA;
+}
+
+template <int IT>
+cudaError_t launch_quantize_rows(const void* X, int T, int K, const int32_t* positions, int copies, int S,
+                                 int8_t* Xq, float* xscale, cudaStream_t st) {
+  const int nchunk = K / 16;
+  const int threads = std::min(expert::kRowThreads, (nchunk + 31) / 32 * 32);
+  const int per = (nchunk + threads - 1) / threads;
+  auto kern = per <= 1   ? expert::quantize_rows_kernel<IT, 1>
+              : per <= 2 ? expert::quantize_rows_kernel<IT, 2>
+                         : expert::quantize_rows_kernel<IT, 0>;
+  return launch(kern, dim3(static_cast<unsigned>(T)), dim3(threads), 0, st, true, X, K, positions, copies, S, Xq,
+                xscale);
+}
+
+int quantize_rows_impl(const void* X, int dtype, int64_t T, int64_t K, const int32_t* positions, int64_t copies,
+                       int64_t S, int8_t* Xq, float* xscale, void* stream) {
+  if (T < 0 || T > INT32_MAX || S < 0 || S > INT32_MAX || K < 16 || K > kMaxK || !float_dtype(dtype))
+    return LLMINT8_ERR_INVALID_ARG;
+  if (positions ? copies < 1 || copies > INT32_MAX : S != T) return LLMINT8_ERR_INVALID_ARG;
+  if (K % 16 != 0) return LLMINT8_ERR_ALIGNMENT;
+  if (T == 0 || S == 0) return LLMINT8_OK;
+  if (!X || !Xq || !xscale) return LLMINT8_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Xq) || misaligned4(xscale) || misaligned4(positions)) return LLMINT8_ERR_ALIGNMENT;
+  const int rc = device_info(nullptr);
+  if (rc != LLMINT8_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int t = static_cast<int>(T), k = static_cast<int>(K), c = static_cast<int>(copies), s = static_cast<int>(S);
+  const cudaError_t e =
+      dtype == LLMINT8_F16    ? launch_quantize_rows<expert::kF16>(X, t, k, positions, c, s, Xq, xscale, st)
+      : dtype == LLMINT8_BF16 ? launch_quantize_rows<expert::kBF16>(X, t, k, positions, c, s, Xq, xscale, st)
+                              : launch_quantize_rows<expert::kF32>(X, t, k, positions, c, s, Xq, xscale, st);
+  return e == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA;
+}
+
+int expert_positions_impl(const void* ids, int id_bytes, int64_t T, int64_t k, int64_t E, int32_t* positions,
+                          int32_t* offsets, void* stream) {
+  if (T < 0 || k < 1 || T > INT32_MAX || k > INT32_MAX || T * k > INT32_MAX - 64) return LLMINT8_ERR_INVALID_ARG;
+  if (E < 1 || E > product::MAX_GROUPS || (id_bytes != 4 && id_bytes != 8)) return LLMINT8_ERR_INVALID_ARG;
+  const int64_t S = T * k;
+  if (!offsets || (S > 0 && (!ids || !positions))) return LLMINT8_ERR_INVALID_ARG;
+  if (misaligned4(positions) || misaligned4(offsets) ||
+      (reinterpret_cast<uintptr_t>(ids) & static_cast<uintptr_t>(id_bytes - 1)))
+    return LLMINT8_ERR_ALIGNMENT;
+  const int rc = device_info(nullptr);
+  if (rc != LLMINT8_OK) return rc;
+  int ctas = 1;
+  while (ctas < expert::kPosMaxCtas && S > static_cast<int64_t>(ctas) * 4 * expert::kPosThreads) ctas *= 2;
+  const int64_t warps = static_cast<int64_t>(ctas) * expert::kPosWarps;
+  const int64_t per_warp = ((S + warps - 1) / warps + 31) / 32 * 32;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t smem = static_cast<size_t>(expert::pos_smem_bytes(static_cast<int>(E)));
+  const int e_ = static_cast<int>(E);
+  const cudaError_t e =
+      id_bytes == 4
+          ? launch_ex(expert::expert_positions_kernel<int32_t>, dim3(ctas), dim3(expert::kPosThreads), smem, st, true,
+                      ctas, static_cast<const int32_t*>(ids), S, e_, per_warp, positions, offsets)
+          : launch_ex(expert::expert_positions_kernel<int64_t>, dim3(ctas), dim3(expert::kPosThreads), smem, st, true,
+                      ctas, static_cast<const int64_t*>(ids), S, e_, per_warp, positions, offsets);
+  return e == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA;
+}
+
+template <int IT, bool VEC>
+auto combine_kernel_for(int out_dtype) {
+  return out_dtype == LLMINT8_F16    ? expert::expert_combine_kernel<IT, expert::kF16, VEC>
+         : out_dtype == LLMINT8_BF16 ? expert::expert_combine_kernel<IT, expert::kBF16, VEC>
+                                     : expert::expert_combine_kernel<IT, expert::kF32, VEC>;
+}
+
+int expert_combine_impl(const void* Y, int y_dtype, int64_t S, int64_t N, const int32_t* positions,
+                        const float* weights, int64_t T, int64_t k, void* out, int out_dtype, void* stream) {
+  if (T < 0 || k < 1 || S < 0 || N < 0 || T > INT32_MAX || k > INT32_MAX || S > INT32_MAX || N > INT32_MAX / 2)
+    return LLMINT8_ERR_INVALID_ARG;
+  if (!float_dtype(y_dtype) || !float_dtype(out_dtype)) return LLMINT8_ERR_INVALID_ARG;
+  if (T == 0 || N == 0) return LLMINT8_OK;
+  if ((!Y && S > 0) || !positions || !weights || !out) return LLMINT8_ERR_INVALID_ARG;
+  if (!aligned16(Y) || !aligned16(out) || misaligned4(positions) || misaligned4(weights))
+    return LLMINT8_ERR_ALIGNMENT;
+  const bool vec = N % 8 == 0;
+  const int64_t cols = (N + (vec ? 8 : 1) * expert::kCombineThreads - 1) / ((vec ? 8 : 1) * expert::kCombineThreads);
+  if (cols > 65535) return LLMINT8_ERR_INVALID_ARG;
+  const int rc = device_info(nullptr);
+  if (rc != LLMINT8_OK) return rc;
+  auto kern = y_dtype == LLMINT8_F16    ? (vec ? combine_kernel_for<expert::kF16, true>(out_dtype)
+                                               : combine_kernel_for<expert::kF16, false>(out_dtype))
+              : y_dtype == LLMINT8_BF16 ? (vec ? combine_kernel_for<expert::kBF16, true>(out_dtype)
+                                               : combine_kernel_for<expert::kBF16, false>(out_dtype))
+                                        : (vec ? combine_kernel_for<expert::kF32, true>(out_dtype)
+                                               : combine_kernel_for<expert::kF32, false>(out_dtype));
+  const cudaError_t e = launch(kern, dim3(static_cast<unsigned>(T), static_cast<unsigned>(cols)),
+                               dim3(expert::kCombineThreads), 0, static_cast<cudaStream_t>(stream), true, Y,
+                               static_cast<int>(S), static_cast<int>(N), positions, weights, static_cast<int>(k), out);
+  return e == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA;
+}
+
 // ------------------------------------------------------------ allocation-free decode
 // Scratch for llmint8_matmul_decode_noalloc: one array per device that loads
 // the library, held until the process exits.  Sized for the decode path's
@@ -934,6 +1174,33 @@ int llmint8_matmul_decode_noalloc(const void* X, int64_t T, int64_t K, const int
                      LLMINT8_PATH_GEMV, Inspect{}, stream);
 }
 
+int llmint8_quantize_rows(const void* X, int dtype, int64_t T, int64_t K, const int32_t* positions, int64_t copies,
+                          int64_t S, int8_t* Xq, float* xscale, void* stream) {
+  return quantize_rows_impl(X, dtype, T, K, positions, copies, S, Xq, xscale, stream);
+}
+
+int llmint8_scaled_matmul(const int8_t* Xq, const float* xscale, int64_t T, int64_t K, const int8_t* Wq,
+                          const float* Wscale, const float* bias, int64_t N, int gated, void* Y, int dtype,
+                          void* stream) {
+  return product_impl(Xq, xscale, T, K, nullptr, false, 1, Wq, Wscale, bias, N, gated, Y, dtype, stream);
+}
+
+int llmint8_grouped_matmul(const int8_t* Xq, const float* xscale, int64_t S, int64_t K, const int32_t* offsets,
+                           int64_t E, const int8_t* Wq, const float* Wscale, const float* bias, int64_t N, int gated,
+                           void* Y, int dtype, void* stream) {
+  return product_impl(Xq, xscale, S, K, offsets, true, E, Wq, Wscale, bias, N, gated, Y, dtype, stream);
+}
+
+int llmint8_expert_positions(const void* ids, int id_bytes, int64_t T, int64_t k, int64_t E, int32_t* positions,
+                             int32_t* offsets, void* stream) {
+  return expert_positions_impl(ids, id_bytes, T, k, E, positions, offsets, stream);
+}
+
+int llmint8_expert_combine(const void* Y, int y_dtype, int64_t S, int64_t N, const int32_t* positions,
+                           const float* weights, int64_t T, int64_t k, void* out, int out_dtype, void* stream) {
+  return expert_combine_impl(Y, y_dtype, S, N, positions, weights, T, k, out, out_dtype, stream);
+}
+
 int llmint8_sync_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return LLMINT8_ERR_CUDA;
@@ -948,7 +1215,7 @@ int llmint8_sync_status(void* stream) {
             cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
       return LLMINT8_ERR_CUDA;
-    return word == kErrBadColumn ? LLMINT8_ERR_INVALID_ARG : LLMINT8_ERR_TIMEOUT;
+    return (word & ~(kErrBadColumn | kErrBadIndex)) == 0 ? LLMINT8_ERR_INVALID_ARG : LLMINT8_ERR_TIMEOUT;
   }
   return LLMINT8_OK;
 }

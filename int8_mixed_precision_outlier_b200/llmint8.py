@@ -63,6 +63,11 @@ def _declare(lib):
         "llmint8_smoothquant_workspace_bytes": (SZ, [I64, I64]),
         "llmint8_smoothquant_matmul": (I, [P, I64, I64, P, P, P, I64, P, P, SZ, P]),
         "llmint8_smoothquant_matmul_debug": (I, [P, I64, I64, P, P, P, I64, P, P, SZ, I, P, P, P, P]),
+        "llmint8_quantize_rows": (I, [P, I, I64, I64, P, I64, I64, P, P, P]),
+        "llmint8_scaled_matmul": (I, [P, P, I64, I64, P, P, P, I64, I, P, I, P]),
+        "llmint8_grouped_matmul": (I, [P, P, I64, I64, P, I64, P, P, P, I64, I, P, I, P]),
+        "llmint8_expert_positions": (I, [P, I, I64, I64, I64, P, P, P]),
+        "llmint8_expert_combine": (I, [P, I, I64, I64, P, P, I64, I64, P, I, P]),
         "llmint8_sync_status": (I, [P]),
         "llmint8_selftest_timeout": (I, [U64, P]),
         "llmint8_set_wait_limit_ns": (I, [U64]),
