@@ -18,6 +18,7 @@ namespace expert {
 using product::kBF16;
 using product::kF16;
 using product::kF32;
+using product::pack_two;
 
 // ------------------------------------------------------------ row quantisation
 // '三、模型量化' (lowentro.cn) Q2, as everywhere in this library: s = max|x| /
@@ -294,17 +295,6 @@ __device__ __forceinline__ float load_one(const void* p, int64_t i) {
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
   else
     return static_cast<const float*>(p)[i];
-}
-
-template <int T>
-__device__ __forceinline__ uint32_t pack_two(float a, float b) {
-  if constexpr (T == kF16) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
 }
 
 // VEC: N % 8 == 0, a thread takes 8 consecutive columns.

@@ -75,17 +75,18 @@ cudaError_t set_attributes() {
 
 // Shared-memory limits of the products with token and channel scales and of
 // the expert positions.
+template <bool PAIR>
 cudaError_t set_product_attributes() {
   cudaError_t e = cudaSuccess;
   auto big = [&](auto kern, int bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  big(product::product_kernel<false, product::kF16>, product::SMEM_BYTES);
-  big(product::product_kernel<false, product::kBF16>, product::SMEM_BYTES);
-  big(product::product_kernel<false, product::kF32>, product::SMEM_BYTES);
-  big(product::product_kernel<true, product::kF16>, product::SMEM_BYTES);
-  big(product::product_kernel<true, product::kBF16>, product::SMEM_BYTES);
-  big(product::product_kernel<true, product::kF32>, product::SMEM_BYTES);
+  big(product::product_kernel<PAIR, false, product::kF16>, product::SMEM_BYTES);
+  big(product::product_kernel<PAIR, false, product::kBF16>, product::SMEM_BYTES);
+  big(product::product_kernel<PAIR, false, product::kF32>, product::SMEM_BYTES);
+  big(product::product_kernel<PAIR, true, product::kF16>, product::SMEM_BYTES);
+  big(product::product_kernel<PAIR, true, product::kBF16>, product::SMEM_BYTES);
+  big(product::product_kernel<PAIR, true, product::kF32>, product::SMEM_BYTES);
   big(expert::expert_positions_kernel<int32_t>, expert::pos_smem_bytes(product::MAX_GROUPS));
   big(expert::expert_positions_kernel<int64_t>, expert::pos_smem_bytes(product::MAX_GROUPS));
   return e;
@@ -109,7 +110,7 @@ int device_info(int* num_sms, int* max_pairs = nullptr) {
       return;
     }
     if (set_attributes<false>() != cudaSuccess || set_attributes<true>() != cudaSuccess ||
-        set_product_attributes() != cudaSuccess) {
+        set_product_attributes<false>() != cudaSuccess || set_product_attributes<true>() != cudaSuccess) {
       d.status = LLMINT8_ERR_CUDA;
       return;
     }
@@ -636,41 +637,57 @@ bool float_dtype(int d) { return d == LLMINT8_F16 || d == LLMINT8_BF16 || d == L
 // ragged groups it plans for equally long ones, and the kernel takes whatever
 // lengths the device's offsets give.
 struct ProductPlan {
-  int BT = 0, box = 0, KPB = 0, H = 0, stages = 0;
+  bool pair = false;
+  int BT = 0, quarter = 0, b_rows = 0, KPB = 0, H = 0, stages = 0, nN = 0;
   int64_t tiles = 0;  // an upper bound
 };
 
-ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, int num_sms) {
+ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, int num_sms, int max_pairs) {
   ProductPlan best;
   const int groups = grouped ? std::min(E, S) : 1;
   const int avg = (S + groups - 1) / groups;
-  const int want = (grouped ? 2 * avg : avg);
-  const int BT = want >= product::MAX_BT ? product::MAX_BT
-                 : want > 64             ? (want + 63) / 64 * 64
-                                         : (want + 15) / 16 * 16;
-  const int box = std::min(BT, 64);
   const bool ksplit = K % product::BK == 0;
-  const int step = gated ? 32 : 8;
-  double best_cost = -1.0;
-  for (int H = step; H <= product::BM; H += step) {
-    const int nN = (N + H - 1) / H;
-    const int64_t tiles = static_cast<int64_t>(groups) * ((avg + BT - 1) / BT) * nN;
-    const double cost = static_cast<double>((tiles + num_sms - 1) / num_sms) * (H + BT + 32);
-    if (best_cost < 0.0 || cost <= best_cost) {
-      best_cost = cost;
-      best.H = H;
-      best.tiles = (static_cast<int64_t>(S) / BT + groups) * nN;
+  const int KB = (K + product::BK - 1) / product::BK;
+  best.pair = avg > 128;
+  const int want = (grouped ? 2 * avg : avg);
+  int BT = want >= product::MAX_BT ? product::MAX_BT : (want + 15) / 16 * 16;
+  best.BT = BT;
+  if (best.pair) {
+    best.H = product::BM;
+    best.nN = (N + 2 * best.H - 1) / (2 * best.H);
+  } else {
+    const int step = gated ? 32 : 8;
+    double best_cost = -1.0;
+    for (int H = step; H <= product::BM; H += step) {
+      const int nN = (N + H - 1) / H;
+      const int64_t tiles = static_cast<int64_t>(groups) * ((avg + BT - 1) / BT) * nN;
+      const double cost = static_cast<double>((tiles + num_sms - 1) / num_sms) * (H + BT + 32);
+      if (best_cost < 0.0 || cost <= best_cost) {
+        best_cost = cost;
+        best.H = H;
+        best.nN = nN;
+      }
     }
   }
-  best.BT = BT;
-  best.box = box;
-  const int rows = best.H + BT;
-  best.KPB = !ksplit || BT > box ? 1 : rows * product::BK * 16 <= product::RING_BYTES ? 4
-             : rows * product::BK * 8 <= product::RING_BYTES ? 2 : 1;
-  best.KPB = std::min(best.KPB, (K + product::BK - 1) / product::BK);
-  if (best.KPB == 3) best.KPB = 2;
-  best.stages = std::min(product::MAX_STAGES, product::RING_BYTES / (rows * product::BK * best.KPB));
+  const int mine = best.pair ? BT / 2 : BT;
+  best.quarter = (mine + 31) / 32 * 8;
+  best.b_rows = (mine + best.quarter - 1) / best.quarter * best.quarter;
+  best.tiles = (static_cast<int64_t>(S) / BT + groups) * best.nN;
+  const int kblock = (best.H + best.b_rows) * product::BK;
+  // at least three stages of as many k-blocks as possible
+  best.KPB = 1;
+  while (ksplit && best.KPB < product::KPB_MAX && 2 * best.KPB <= KB && 3 * 2 * best.KPB * kblock <= product::RING_BYTES)
+    best.KPB *= 2;
+  best.stages = std::min(product::MAX_STAGES, product::RING_BYTES / (kblock * best.KPB));
   return best;
+}
+
+using ProductKernel = void (*)(const CUtensorMap, const product::TokenMaps, const product::Params);
+template <bool PAIR, bool GATED>
+ProductKernel product_kernel_for(int dtype) {
+  return dtype == LLMINT8_F16    ? product::product_kernel<PAIR, GATED, product::kF16>
+         : dtype == LLMINT8_BF16 ? product::product_kernel<PAIR, GATED, product::kBF16>
+                                 : product::product_kernel<PAIR, GATED, product::kF32>;
 }
 
 int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const int32_t* offsets, bool grouped,
@@ -685,11 +702,11 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || misaligned4(sx) || misaligned4(sw) ||
       misaligned4(bias) || misaligned4(offsets))
     return LLMINT8_ERR_ALIGNMENT;
-  int num_sms = 0;
-  const int rc = device_info(&num_sms);
+  int num_sms = 0, max_pairs = 0;
+  const int rc = device_info(&num_sms, &max_pairs);
   if (rc != LLMINT8_OK) return rc;
   const ProductPlan plan = plan_product(static_cast<int>(S), static_cast<int>(N), static_cast<int>(K),
-                                        static_cast<int>(E), grouped, gated != 0, num_sms);
+                                        static_cast<int>(E), grouped, gated != 0, num_sms, max_pairs);
   if (plan.tiles > INT32_MAX) return LLMINT8_ERR_INVALID_ARG;
   product::Params p;
   p.S = static_cast<int>(S);
@@ -703,9 +720,10 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   p.NU = (p.KB + p.KPB - 1) / p.KPB;
   p.ksplit = K % product::BK == 0 ? 1 : 0;
   p.H = plan.H;
-  p.nN = (p.N + p.H - 1) / p.H;
+  p.nN = plan.nN;
   p.BT = plan.BT;
-  p.box = plan.box;
+  p.quarter = plan.quarter;
+  p.b_rows = plan.b_rows;
   p.stages = plan.stages;
   p.sx = sx;
   p.sw = sw;
@@ -718,24 +736,21 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   const cuuint64_t k1 = p.ksplit ? static_cast<cuuint64_t>(K / product::BK) : 1;
   const cuuint64_t Ku = static_cast<cuuint64_t>(K), Nu = static_cast<cuuint64_t>(N), Eu = static_cast<cuuint64_t>(E);
   const cuuint32_t kpb = static_cast<cuuint32_t>(p.KPB), H = static_cast<cuuint32_t>(p.H);
-  CUtensorMap tw, tx;
-  const bool ok =
-      (gated ? encode_tiled<5>(&tw, Wq, {k0, 16, 2 * Eu, Nu / 32, k1}, {Ku, Nu / 2 * Ku, 16 * Ku, product::BK},
-                               {product::BK, 16, 2, H / 32, kpb})
-             : encode_tiled<4>(&tw, Wq, {k0, Nu, k1, Eu}, {Ku, product::BK, Nu * Ku}, {product::BK, H, kpb, 1})) &&
-      encode_tiled<3>(&tx, Xq, {k0, static_cast<cuuint64_t>(S), k1}, {Ku, product::BK},
-                      {product::BK, static_cast<cuuint32_t>(p.box), kpb});
+  CUtensorMap tw;
+  product::TokenMaps tx;
+  bool ok = gated ? encode_tiled<5>(&tw, Wq, {k0, 16, 2 * Eu, Nu / 32, k1}, {Ku, Nu / 2 * Ku, 16 * Ku, product::BK},
+                                    {product::BK, 16, 2, H / 32, kpb})
+                  : encode_tiled<4>(&tw, Wq, {k0, Nu, k1, Eu}, {Ku, product::BK, Nu * Ku}, {product::BK, H, kpb, 1});
+  for (int i = 0; ok && i < 4; ++i)
+    ok = encode_tiled<3>(&tx.m[i], Xq, {k0, static_cast<cuuint64_t>(S), k1}, {Ku, product::BK},
+                         {product::BK, static_cast<cuuint32_t>(std::min((i + 1) * p.quarter, p.b_rows)), kpb});
   if (!ok) return LLMINT8_ERR_CUDA;
-  void (*kern)(const CUtensorMap, const CUtensorMap, const product::Params) =
-      gated ? (dtype == LLMINT8_F16    ? product::product_kernel<true, product::kF16>
-               : dtype == LLMINT8_BF16 ? product::product_kernel<true, product::kBF16>
-                                       : product::product_kernel<true, product::kF32>)
-            : (dtype == LLMINT8_F16    ? product::product_kernel<false, product::kF16>
-               : dtype == LLMINT8_BF16 ? product::product_kernel<false, product::kBF16>
-                                       : product::product_kernel<false, product::kF32>);
-  const int grid = static_cast<int>(std::min<int64_t>(num_sms, plan.tiles));
-  const cudaError_t e = launch(kern, dim3(grid), dim3(product::THREADS), product::SMEM_BYTES,
-                               static_cast<cudaStream_t>(stream), true, tw, tx, p);
+  const ProductKernel kern = plan.pair ? (gated ? product_kernel_for<true, true>(dtype) : product_kernel_for<true, false>(dtype))
+                                       : (gated ? product_kernel_for<false, true>(dtype) : product_kernel_for<false, false>(dtype));
+  const int units = static_cast<int>(std::min<int64_t>(plan.pair ? max_pairs : num_sms, plan.tiles));
+  const cudaError_t e = launch_ex(kern, dim3(plan.pair ? 2 * units : units), dim3(product::THREADS),
+                                  product::SMEM_BYTES, static_cast<cudaStream_t>(stream), true, plan.pair ? 2 : 1, tw,
+                                  tx, p);
   return e == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA;
 }
 

@@ -17,8 +17,8 @@
 // 15 columns instead of a 128-row tile, and few tokens cost few columns, which
 // leaves short groups bound by reading the weights.
 //
-// One persistent CTA per SM walks the tiles w = blockIdx.x, + gridDim.x, ...;
-// tile w belongs to the group whose cumulative tile count covers it, found in
+// One persistent CTA per SM (or a pair of CTAs on two) walks the tiles w =
+// unit, + units, ...; tile w belongs to the group whose cumulative tile count covers it, found in
 // shared memory from the device's offsets (the host never waits for them).
 // Warp 0 copies (TMA, 128-byte swizzle), warp 1 issues tcgen05.mma kind::i8
 // and owns TMEM, warps 2-9 write the results.  Two 256-column accumulators
@@ -42,9 +42,12 @@ constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 512;     // two accumulators of MAX_BT columns
 constexpr int RING_BYTES = 192 * 1024;  // stages, and 16 KiB past the last one (see SLACK)
-// A tile of fewer than 128 weight rows is multiplied as 128: the lanes past
-// its end read whatever follows in shared memory and are never stored.
-constexpr int SLACK_BYTES = BM * BK;
+// Behind the ring: the epilogue's staging.  A tile of fewer than 128 weight
+// rows is multiplied as 128, and the lanes past its end (never stored) read
+// whatever follows in shared memory: after the last stage, these 16 KiB.
+constexpr int STAGING_BYTES = 8 * 1024;       // of one set of 4 epilogue warps
+constexpr int SLACK_BYTES = 2 * STAGING_BYTES;
+static_assert(SLACK_BYTES >= BM * BK, "the last stage's 128 rows end inside shared memory");
 constexpr int SX_BYTES = 2 * MAX_BT * 4;
 constexpr int GROUP_BYTES = 2 * (MAX_GROUPS + 1) * 4;
 constexpr int BAR_BYTES = 512;
@@ -60,16 +63,24 @@ struct Params {
   const int32_t* offsets;  // [E + 1] on the device, null: one group [0, S)
   int KB, KPB, NU;     // k-blocks, k-blocks per stage, stages per tile
   int ksplit;          // 1: the copies see K as [K / 128][128] (K % 128 == 0); 0: as one row, KPB = 1
-  int H;               // weight rows of a tile (a multiple of 8; of 32 when gated)
-  int nN;              // tiles along the channels
+  int H;               // weight rows of a tile and CTA (a multiple of 8; of 32 when gated)
+  int nN;              // tiles along the channels (2 H rows each for CTA pairs)
   int BT;              // most tokens of a tile, a multiple of 16
-  int box;             // token rows of one copy; BT is a multiple of it
+  int quarter;         // token rows of a copy come in 1..4 quarters (a multiple of 8 rows each)
+  int b_rows;          // token rows that a k-block of a stage has room for
   int stages;
   const float* sx;
   const float* sw;
   const float* bias;   // null: none
   void* Y;
   uint64_t wait_ns;
+};
+
+// Copies of token rows 1, 2, 3 or 4 quarters high, so that a short tile does
+// not fetch a full one's rows and every stage still takes one copy of each
+// operand (a second one costs the producer about as much as 16 KiB of data).
+struct TokenMaps {
+  CUtensorMap m[4];
 };
 
 // A tile: `tok` tokens from row m0 of Xq / Y, weight rows (or gated channel
@@ -171,12 +182,152 @@ __device__ __forceinline__ void store_out(void* Y, int64_t i, float v) {
     static_cast<float*>(Y)[i] = v;
 }
 
+// Two values rounded to a 16-bit type, the first in the low half.
+template <int OT>
+__device__ __forceinline__ uint32_t pack_two(float a, float b) {
+  if constexpr (OT == kF16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// ------------------------------------------------------------ epilogue
+// The accumulator has channels along the TMEM lanes and tokens along the
+// columns; Y has channels along its rows.  A set of 4 warps turns CHUNK tokens
+// by all channels of the tile around through shared memory, so that Y is
+// written 16 bytes a thread in whole runs of the tile's channels.  (Storing
+// each lane's channel directly, 64 bytes per warp and token, took 9.7 us per
+// tile of 128 x 256 against 3.3 us of products at K = 1408.)
+//
+// tcgen05.ld 16x256b gives a thread two tokens of one channel per register
+// pair: the shape that stmatrix.trans stores 8 channels of a token from.  In
+// a gated tile TMEM lanes 0-15 of a quadrant hold the gates and lanes 16-31 the
+// values of the same 16 channels, so both halves of an output meet in a thread.
+//
+// Staging layout: [token][channel], the 16-byte (16-bit types: chunk index ^
+// token % 8; binary32: word index ^ 8 (token / 2 % 4)) position swizzled so
+// that neither the writes nor the reads meet in a bank.
+template <bool GATED, int OT>
+struct Epilogue {
+  static constexpr bool k32 = OT == kF32;
+  static constexpr int CH = GATED ? BM / 2 : BM;             // channels of a CTA's tile
+  static constexpr int ROW_BYTES = CH * (k32 ? 4 : 2);
+  static constexpr int CHUNK = k32 && !GATED ? 16 : 32;      // tokens staged at a time
+  static constexpr int VEC = k32 ? 4 : 8;                    // elements in 16 bytes
+  static_assert(CHUNK * ROW_BYTES <= STAGING_BYTES, "staging");
+
+  __device__ static uint32_t at(int token, int channel) {    // byte offset in the staging
+    if constexpr (k32) return token * ROW_BYTES + ((channel ^ (((token >> 1) & 3) << 3)) << 2);
+    const int chunk = (channel >> 3) ^ (token & 7);
+    return token * ROW_BYTES + (chunk << 4) + ((channel & 7) << 1);
+  }
+
+  // Outputs of CHUNK columns, staged by this warp.  `sw`, `b`: of TMEM lanes l / 4 + {0, 8, 16, 24} of the quadrant.
+  __device__ static void stage(uint8_t* st, uint32_t addr, int q, int lane, const float* sx, const float (&sw)[4],
+                               const float (&b)[4]) {
+    uint32_t lo[CHUNK / 2], hi[CHUNK / 2];  // TMEM lanes 0-15 and 16-31
+    [[maybe_unused]] uint32_t keep0 = 0, keep1 = 0;
+    tmem_ld_16lanes(addr, lo);
+    tmem_ld_16lanes(addr + (16u << 16), hi);
+    tmem_ld_wait();
+    tmem_regs_ready(lo);
+    tmem_regs_ready(hi);
+    const int r = lane >> 2, col = 2 * (lane & 3);
+    auto z = [](uint32_t acc, float sxv, float swv, float bv) {
+      return static_cast<float>(static_cast<int32_t>(acc)) * sxv * swv + bv;
+    };
+#pragma unroll
+    for (int i = 0; i < CHUNK / 8; ++i) {  // 8 tokens each
+      const float2 s = *reinterpret_cast<const float2*>(sx + 8 * i + col);
+      float y[4][2];  // [channel block of 8][token]
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float sv = h ? s.y : s.x;
+        const float z0 = z(lo[4 * i + h], sv, sw[0], b[0]), z1 = z(lo[4 * i + 2 + h], sv, sw[1], b[1]);
+        const float z2 = z(hi[4 * i + h], sv, sw[2], b[2]), z3 = z(hi[4 * i + 2 + h], sv, sw[3], b[3]);
+        if constexpr (GATED) {
+          y[0][h] = gate(z0, z2);
+          y[1][h] = gate(z1, z3);
+        } else {
+          y[0][h] = z0;
+          y[1][h] = z1;
+          y[2][h] = z2;
+          y[3][h] = z3;
+        }
+      }
+      constexpr int NB = GATED ? 2 : 4;  // channel blocks of this warp
+      if constexpr (k32) {
+#pragma unroll
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float*>(st + at(8 * i + col + h, (q * NB + c) * 8 + r)) = y[c][h];
+      } else if constexpr (GATED) {
+        // two channel blocks of 8 tokens: the second pair of matrices is the
+        // next 8 tokens', held back until they are there
+        if (i & 1) {
+          const int m = lane >> 3, j = lane & 7;  // matrix and token of this lane's address
+          stmatrix_x4_trans(smem_addr(st) + at(8 * (i - 1 + (m >> 1)) + j, (q * 2 + (m & 1)) * 8), keep0, keep1,
+                            pack_two<OT>(y[0][0], y[0][1]), pack_two<OT>(y[1][0], y[1][1]));
+        } else {
+          keep0 = pack_two<OT>(y[0][0], y[0][1]);
+          keep1 = pack_two<OT>(y[1][0], y[1][1]);
+        }
+      } else {
+        const int m = lane >> 3, j = lane & 7;
+        stmatrix_x4_trans(smem_addr(st) + at(8 * i + j, (q * 4 + m) * 8), pack_two<OT>(y[0][0], y[0][1]),
+                          pack_two<OT>(y[1][0], y[1][1]), pack_two<OT>(y[2][0], y[2][1]),
+                          pack_two<OT>(y[3][0], y[3][1]));
+      }
+    }
+  }
+
+  // The staged tokens to Y rows m .., channels c .. c + n - 1 (n <= CH), by
+  // the 128 threads of the set.
+  __device__ static void write(const uint8_t* st, void* Y, int No, int64_t m, int cnt, int c, int n, int tid) {
+    constexpr int PER_ROW = CH / VEC, ROWS = 128 / PER_ROW;
+    constexpr int SIZE = k32 ? 4 : 2;
+    uint8_t* y = static_cast<uint8_t*>(Y);
+    if (No % VEC == 0) {  // n is a multiple of VEC too
+      const int v = (tid % PER_ROW) * VEC;
+      if (v < n) {
+#pragma unroll
+        for (int t0 = 0; t0 < CHUNK; t0 += ROWS) {
+          const int t = t0 + tid / PER_ROW;
+          if (t < cnt)
+            *reinterpret_cast<uint4*>(y + ((m + t) * No + c + v) * SIZE) =
+                *reinterpret_cast<const uint4*>(st + at(t, v));
+        }
+      }
+    } else {
+      for (int i = tid; i < cnt * CH; i += 128) {
+        const int t = i / CH, v = i % CH;
+        if (v < n) {
+          if constexpr (k32)
+            reinterpret_cast<float*>(y)[(m + t) * No + c + v] = *reinterpret_cast<const float*>(st + at(t, v));
+          else
+            reinterpret_cast<uint16_t*>(y)[(m + t) * No + c + v] = *reinterpret_cast<const uint16_t*>(st + at(t, v));
+        }
+      }
+    }
+  }
+};
+
 // GATED: the weight copies interleave 16 gate rows with the 16 value rows of
 // the same channels, so that lanes l and l + 16 of a warp hold the two halves
 // of one output.  OT: output type.
-template <bool GATED, int OT>
+//
+// PAIR: a 2-CTA cluster works on one tile of 2 H weight rows (tcgen05
+// cta_group::2, M = 256): CTA r holds weight rows H r .. of the tile and half
+// of its tokens as operands, and after the products H rows by all tokens in
+// its TMEM.  The even CTA's thread issues the MMAs; both CTAs' copies complete
+// on its `full` barriers, and each commit arrives at both CTAs.
+template <bool PAIR, bool GATED, int OT>
 __global__ void __launch_bounds__(THREADS, 1)
-    product_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+    product_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ TokenMaps tmaps_x,
                    const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -193,25 +344,33 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int units = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmap_w);
-    prefetch_tensormap(&tmap_x);
+    for (int i = 0; i < 4; ++i) prefetch_tensormap(&tmaps_x.m[i]);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], EPI_WARPS);
+      mbar_init(&tempty[b], (PAIR ? 2 : 1) * EPI_WARPS);
     }
     mbar_init(done, 1);
     fence_barrier_init();
   }
   __syncwarp();
   if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   // The codes, scales and offsets may come from the kernel before this one,
   // and so may the weights (a user may have quantised them just now): nothing
@@ -221,154 +380,210 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_launch_dependents();
   if (warp == 2) scan_groups(p, off, cum);
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if constexpr (PAIR)
+    cluster_sync();  // both CTAs' barriers are initialised before a copy or commit reaches them
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = cum[p.E];
-  const int a_bytes = p.H * BK, b_bytes = p.BT * BK;  // of one k-block
+  const int a_bytes = p.H * BK;                     // of one k-block
+  const int b_bytes = p.b_rows * BK;
   const int stage_bytes = (a_bytes + b_bytes) * p.KPB;
   auto stage_b = [&](int s) { return smem + s * stage_bytes; };
   auto stage_a = [&](int s) { return smem + s * stage_bytes + p.KPB * b_bytes; };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-        const Tile t = find_tile(p, off, cum, w);
-        const int boxes = (t.tok + p.box - 1) / p.box;
-        const uint32_t tx = static_cast<uint32_t>(p.KPB * (a_bytes + boxes * p.box * BK));
-        for (int u = 0; u < p.NU; ++u, ++it) {
-          const int s = it % p.stages;
-          if (it >= p.stages &&
-              !mbar_wait(&empty[s], ((it / p.stages) & 1) ^ 1, p.wait_ns, kErrTimeoutProducer)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full[s], tx);
+    // All lanes walk the loop, one issues: its addresses and coordinates are
+    // then uniform values.  (With the loop inside `if (lane == 0)` an MMA took
+    // 71 cycles to issue and a stage 300 more, whatever its size.)
+    const bool issuer = elect_one();
+    int it = 0, s = 0;      // stages filled so far; the stage to fill next
+    uint32_t phase = 1;     // parity its `empty` barrier had before this round (passes at once in round 0)
+    bool ok = true;
+    for (int w = unit; ok && w < total; w += units) {
+      const Tile t = find_tile(p, off, cum, w);
+      const int cols = (t.tok + 15) / 16 * 16;     // MMA N
+      const int mine = PAIR ? cols / 2 : cols;     // token rows this CTA copies
+      const int x0 = t.m0 + rank * mine;
+      const int quarters = (mine + p.quarter - 1) / p.quarter;
+      const CUtensorMap* tmap_x = &tmaps_x.m[quarters - 1];
+      const int wt = PAIR ? 2 * t.nt + rank : t.nt;  // this CTA's weight rows, in units of H
+      const uint32_t tx = static_cast<uint32_t>((PAIR ? 2 : 1) * p.KPB * (a_bytes + quarters * p.quarter * BK));
+      for (int u = 0; u < p.NU; ++u, ++it) {
+        ok = mbar_wait_stage(&empty[s], phase, p.wait_ns, kErrTimeoutProducer);
+        if (!ok) break;
+        if (issuer) {
           const int kb = p.ksplit ? u * p.KPB : 0, x = p.ksplit ? 0 : u * BK;
-          if constexpr (GATED)
-            tma_load_5d(stage_a(s), &tmap_w, &full[s], x, 0, 2 * t.e, t.nt * (p.H / 32), kb);
-          else
-            tma_load_4d(stage_a(s), &tmap_w, &full[s], x, t.nt * p.H, kb, t.e);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_3d(stage_b(s) + b * p.box * BK, &tmap_x, &full[s], x, t.m0 + b * p.box, kb);
+          if constexpr (PAIR) {
+            const uint32_t bar = map_shared_rank(&full[s], 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
+            if constexpr (GATED)
+              tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.e, wt * (p.H / 32), kb);
+            else
+              tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.e);
+            tma_load_3d_pair(stage_b(s), tmap_x, bar, x, x0, kb);
+          } else {
+            mbar_arrive_expect_tx(&full[s], tx);
+            if constexpr (GATED)
+              tma_load_5d(stage_a(s), &tmap_w, &full[s], x, 0, 2 * t.e, wt * (p.H / 32), kb);
+            else
+              tma_load_4d(stage_a(s), &tmap_w, &full[s], x, wt * p.H, kb, t.e);
+            tma_load_3d(stage_b(s), tmap_x, &full[s], x, x0, kb);
+          }
+        }
+        if (++s == p.stages) {
+          s = 0;
+          phase ^= 1;
         }
       }
-      // Leave no copy in flight: wait for the last loads of every stage.
-      for (int i = it < p.stages ? 0 : it - p.stages; i < it; ++i)
-        mbar_wait(&full[i % p.stages], (i / p.stages) & 1, p.wait_ns, kErrTimeoutProducer);
+    }
+    // Leave no copy in flight: wait for the last loads of every stage (in a
+    // pair the `done` commit covers the copies of both CTAs).
+    if constexpr (!PAIR) {
+      for (int i = min(it, p.stages); i > 0; --i) {
+        if (--s < 0) {
+          s = p.stages - 1;
+          phase ^= 1;
+        }
+        mbar_wait_stage(&full[s], phase ^ 1, p.wait_ns, kErrTimeoutProducer);
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int it = 0, tc = 0;
+    const bool issuer = elect_one();
+    if (rank == 0) {
+      const uint32_t ring = smem_addr(smem);
+      int s = 0, tc = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += gridDim.x, ++tc) {
+      for (int w = unit; ok && w < total; w += units, ++tc) {
         const Tile t = find_tile(p, off, cum, w);
-        const uint32_t idesc = idesc_i8_s32(BM, (t.tok + 15) / 16 * 16);
+        const int cols = (t.tok + 15) / 16 * 16;
+        const uint32_t idesc = idesc_i8_s32(PAIR ? 2 * BM : BM, cols);
+        // k-blocks of a stage lie as the copy put them: its rows apart
+        const uint32_t b_step =
+            static_cast<uint32_t>(((PAIR ? cols / 2 : cols) + p.quarter - 1) / p.quarter * p.quarter * BK) >> 4;
         const int buf = tc & 1;
         if (tc >= 2) {
-          ok = mbar_wait(&tempty[buf], ((tc >> 1) - 1) & 1, p.wait_ns, kErrTimeoutMma);
+          ok = mbar_wait_stage<PAIR>(&tempty[buf], ((tc >> 1) - 1) & 1, p.wait_ns, kErrTimeoutMma);
           if (!ok) break;
         }
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(buf * MAX_BT);
-        for (int u = 0; u < p.NU; ++u, ++it) {
-          const int s = it % p.stages;
-          ok = mbar_wait(&full[s], (it / p.stages) & 1, p.wait_ns, kErrTimeoutMma);
+        for (int u = 0; u < p.NU; ++u) {
+          ok = mbar_wait_stage(&full[s], phase, p.wait_ns, kErrTimeoutMma);
           if (!ok) break;
           tc_fence_after();
-          const int nkb = min(p.KPB, p.KB - u * p.KPB);
-          for (int j = 0; j < nkb; ++j) {
-            const uint32_t a0 = smem_addr(stage_a(s)) + static_cast<uint32_t>(j * a_bytes);
-            const uint32_t b0 = smem_addr(stage_b(s)) + static_cast<uint32_t>(j * b_bytes);
+          if (issuer) {
+            const int nkb = min(p.KPB, p.KB - u * p.KPB);
+            uint32_t blow = sdesc_low(ring + s * stage_bytes);
+            uint32_t alow = sdesc_low(ring + s * stage_bytes + p.KPB * b_bytes);
+            for (int j = 0; j < nkb; ++j, alow += a_bytes >> 4, blow += b_step) {
+              mma_i8_low<PAIR>(d, alow, blow, idesc, (u > 0 || j > 0) ? 1u : 0u);
 #pragma unroll
-            for (int k = 0; k < BK / 32; ++k)
-              mma_i8(d, make_sdesc_k_sw128(a0 + k * 32), make_sdesc_k_sw128(b0 + k * 32), idesc,
-                     (u > 0 || j > 0 || k > 0) ? 1u : 0u);
+              for (int k = 1; k < BK / 32; ++k) mma_i8_low<PAIR>(d, alow + 2 * k, blow + 2 * k, idesc, 1u);
+            }
+            if constexpr (PAIR)
+              mma_commit_pair(&empty[s], 0x3);
+            else
+              mma_commit(&empty[s]);
           }
-          mma_commit(&empty[s]);
+          if (++s == p.stages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        if (ok) mma_commit(&tfull[buf]);
+        if (ok && issuer) {
+          if constexpr (PAIR)
+            mma_commit_pair(&tfull[buf], 0x3);
+          else
+            mma_commit(&tfull[buf]);
+        }
       }
-      mma_commit(done);
-      mbar_wait(done, 0, p.wait_ns, kErrTimeoutMma);
+      if (issuer) {
+        if constexpr (PAIR)
+          mma_commit_pair(done, 0x3);
+        else
+          mma_commit(done);
+      }
     }
+    // The MMAs (of both CTAs) are complete before TMEM is released.
+    mbar_wait_stage(done, 0, p.wait_ns, kErrTimeoutMma);
   } else {
     // ------------------------------------------------------------ epilogue
+    using Epi = Epilogue<GATED, OT>;
     const int q = warp & 3;                   // TMEM lane quadrant of this warp
     const int set = (warp - 2) >> 2;          // two sets of 4 warps share the columns
     const int etid = static_cast<int>(threadIdx.x) - 64;
-    const int row = q * 32 + lane;            // row of the tile = TMEM lane
+    const int stid = etid & 127;
+    const uint32_t set_bar = 2u + static_cast<uint32_t>(set);
+    uint8_t* staging = smem + RING_BYTES + set * STAGING_BYTES;
+    const int tile_ch = GATED ? p.H / 2 : p.H;  // channels of this CTA's tile
     int tc = 0;
-    for (int w = blockIdx.x; w < total; w += gridDim.x, ++tc) {
+    for (int w = unit; w < total; w += units, ++tc) {
       const Tile t = find_tile(p, off, cum, w);
       const int buf = tc & 1;
       float* sxb = sx_s + buf * MAX_BT;
       // The buffer's readers two tiles ago are past the previous tile's barrier.
       for (int j = etid; j < t.tok; j += 32 * EPI_WARPS) sxb[j] = p.sx[t.m0 + j];
-      // This lane's weight row n and output column c (past the end: not stored).
-      int n, c;
-      if constexpr (GATED) {
-        c = t.nt * (p.H / 2) + q * 16 + (lane & 15);
-        n = c + (lane >> 4) * p.No;
-      } else {
-        n = c = t.nt * p.H + row;
+      const int c = (PAIR ? 2 * t.nt + rank : t.nt) * tile_ch;  // first channel
+      const int n = min(tile_ch, p.No - c);                     // channels inside Y (<= 0: none)
+      float sw[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // TMEM lanes l / 4 + 8 i of the quadrant
+        const int ch = GATED ? q * 16 + (lane >> 2) + 8 * (i & 1) : q * 32 + (lane >> 2) + 8 * i;
+        const int64_t at = static_cast<int64_t>(t.e) * p.N + c + ch + (GATED && i >= 2 ? p.No : 0);
+        sw[i] = ch < n ? p.sw[at] : 0.0f;
+        b[i] = ch < n && p.bias ? p.bias[at] : 0.0f;
       }
-      const bool mine = row < p.H && c < p.No;
-      const int64_t at = static_cast<int64_t>(t.e) * p.N + n;
-      const float sw = mine ? p.sw[at] : 0.0f;
-      const float b = mine && p.bias ? p.bias[at] : 0.0f;
-      const bool ok = mbar_wait(&tfull[buf], (tc >> 1) & 1, p.wait_ns, kErrTimeoutEpilogue);
+      // One thread polls, the others sleep at the barrier.
+      const bool ok = etid != 0 || mbar_wait_stage(&tfull[buf], (tc >> 1) & 1, p.wait_ns, kErrTimeoutEpilogue);
       if (!named_barrier_and(1, 32 * EPI_WARPS, ok)) break;  // also: sxb is written
       tc_fence_after();
       const uint32_t addr =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * MAX_BT);
-      if (q * 32 < p.H) {
-        for (int c0 = set * 32; c0 < t.tok; c0 += 64) {
-          uint32_t r[32];
-          tmem_ld32(addr + c0, r);
-          tmem_ld_wait();
-          tmem_regs_ready(r);
-          const int cnt = min(32, t.tok - c0);
-          if constexpr (GATED) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float v0 = static_cast<float>(static_cast<int32_t>(r[j])) * sxb[c0 + j] * sw + b;
-              const float v1 = static_cast<float>(static_cast<int32_t>(r[j + 1])) * sxb[c0 + j + 1] * sw + b;
-              // Lane l < 16 keeps its gate of column j and takes the value
-              // from lane l + 16, which takes the gate of column j + 1.
-              const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? v1 : v0, 16);
-              const float y = lane < 16 ? gate(v0, other) : gate(other, v1);
-              const int jj = j + (lane >> 4);
-              if (mine && jj < cnt) store_out<OT>(p.Y, static_cast<int64_t>(t.m0 + c0 + jj) * p.No + c, y);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float y = static_cast<float>(static_cast<int32_t>(r[j])) * sxb[c0 + j] * sw + b;
-              if (mine && j < cnt) store_out<OT>(p.Y, static_cast<int64_t>(t.m0 + c0 + j) * p.No + c, y);
-            }
-          }
+      if (n > 0) {
+        for (int c0 = set * Epi::CHUNK; c0 < t.tok; c0 += 2 * Epi::CHUNK) {
+          if (c0 >= 2 * Epi::CHUNK) named_barrier(set_bar, 128);  // the staging has been read
+          Epi::stage(staging, addr + c0, q, lane, sxb + c0, sw, b);
+          named_barrier(set_bar, 128);
+          Epi::write(staging, p.Y, p.No, t.m0 + c0, min(Epi::CHUNK, t.tok - c0), c, n, stid);
         }
       }
       // This warp has read its columns: the MMAs of the tile after next may
-      // write them.
+      // write them.  (The next tile's barrier keeps the staging until all of
+      // the set has read it.)
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[buf]);
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_cluster(map_shared_rank(&tempty[buf], 0));
+        else
+          mbar_arrive(&tempty[buf]);
+      }
     }
   }
 
-  // Bring the warps whose lane 0 ran a role back together before the barrier.
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) {
+    // Neither CTA leaves while the other may still signal its barriers or,
+    // after a timeout, copies of the pair may still be landing.
+    if (threadIdx.x == 0 && ld_error_word() != 0) sleep_ns_bounded(20000);
+    __syncwarp();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, TMEM_COLS);
   }
 }
 

@@ -5,71 +5,69 @@ that go with them (include/llmint8.h).
 Argument marshalling only, as llmint8.py: dtypes, shapes, devices and layouts
 are checked, outputs that are not given are allocated on the call's stream, and
 the library's kernels do the rest.  Calls run on the device of their tensors,
-whichever is current.
+whichever is current.  For few tokens the host's time is what a call costs, so
+each operand is checked by one test of all its properties, which is taken apart
+only to name what is wrong.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
-from .llmint8 import _check, _need, llmint8_quantize_weight, load_library
+from .llmint8 import _check, _need, load_library
 
-_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_F16, _BF16, _F32, _I8, _I32 = torch.float16, torch.bfloat16, torch.float32, torch.int8, torch.int32
+_DTYPES = {_F16: 0, _BF16: 1, _F32: 2}
 MAX_EXPERTS = 1024
 
-
-def _same_device(first: torch.Tensor, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+_Tensor = torch.Tensor
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the pointer alone: 3 us less than a Stream object
 
 
-def _shape(t: torch.Tensor, shape: tuple, name: str):
-    if t.shape != shape:
+def _refuse(t, dtype, shape, name, index):
+    """Raises for what is wrong with an operand (see _operand)."""
+    _need(t, dtype, len(shape), name)
+    if tuple(t.shape) != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _float(t, ndim: int, name: str):
-    if isinstance(t, torch.Tensor) and t.dtype not in _DTYPES:
+def _operand(t, dtype, shape, name, index):
+    """A contiguous CUDA tensor of this type and shape on device `index`."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        _refuse(t, dtype, shape, name, index)
+
+
+def _first(t, dtypes, ndim, name) -> int:
+    """The device of a call's first operand; `dtypes` None: any of the float types."""
+    if isinstance(t, _Tensor) and dtypes is None and t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
-    _need(t, t.dtype if isinstance(t, torch.Tensor) else None, ndim, name)
+    if isinstance(t, _Tensor) and dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, got {t.dtype}")
+    if not (isinstance(t, _Tensor) and t.is_cuda and t.dim() == ndim and t.is_contiguous()):
+        _need(t, t.dtype if isinstance(t, _Tensor) else None, ndim, name)
+    return t.get_device()
 
 
 def _out_dtype(dtype) -> int:
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"dtype must be float16, bfloat16 or float32, got {dtype}")
-    return _DTYPES[dtype]
+    return code
 
 
-class _On:
-    """The tensors' device and the call's stream, current while outputs are
-    allocated and kernels launched (an output belongs to the stream that
-    writes it)."""
-
-    __slots__ = ("guard", "stream")
-
-    def __init__(self, device: torch.device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self.guard = None
-        if stream is not None:
-            self.guard = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-            stream = torch.cuda.current_stream(device)
-        else:
-            stream = torch.cuda.current_stream()
-        self.stream = stream.cuda_stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return ctypes.c_void_p(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _run(index: int, stream, call):
+    """call(pointer of the stream) with the tensors' device and the call's
+    stream current, so that an output belongs to the stream that writes it."""
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return call(_raw_stream(index))
+        with torch.cuda.device(index):
+            return call(_raw_stream(index))
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def llmint8_quantize_rows(X: torch.Tensor, positions: torch.Tensor | None = None, Xq: torch.Tensor | None = None,
@@ -82,74 +80,77 @@ def llmint8_quantize_rows(X: torch.Tensor, positions: torch.Tensor | None = None
     Xq is given, and rows that no position names are left as they were.
     Positions must be distinct.  A row with a NaN or an infinity gets the scale
     NaN and codes 0."""
-    _float(X, 2, "X")
+    index = _first(X, None, 2, "X")
     T, K = X.shape
-    copies = 0
-    S = T
+    copies, S, at = 0, T, None
     if positions is not None:
-        _need(positions, torch.int32, 2, "positions")
+        _first(positions, (_I32,), 2, "positions")
         copies = positions.shape[1]
-        _shape(positions, (T, copies), "positions")
+        _operand(positions, _I32, (T, copies), "positions", index)
         if copies < 1:
             raise ValueError("positions must have a column")
-        S = T * copies if Xq is None else Xq.shape[0]
-    with _On(X.device, stream) as st:
-        Xq = torch.empty((S, K), dtype=torch.int8, device=X.device) if Xq is None else Xq
-        xscale = torch.empty(S, dtype=torch.float32, device=X.device) if xscale is None else xscale
-        _need(Xq, torch.int8, 2, "Xq")
-        _need(xscale, torch.float32, 1, "xscale")
-        _shape(Xq, (S, K), "Xq")
-        _shape(xscale, (S,), "xscale")
-        _same_device(X, positions=positions, Xq=Xq, xscale=xscale)
-        _check(load_library().llmint8_quantize_rows(
-            X.data_ptr(), _DTYPES[X.dtype], T, K, None if positions is None else positions.data_ptr(), copies, S,
-            Xq.data_ptr(), xscale.data_ptr(), st), "llmint8_quantize_rows")
-    return Xq, xscale
+        at = positions.data_ptr()
+        S = T * copies
+        if Xq is not None:
+            _first(Xq, (_I8,), 2, "Xq")
+            S = Xq.shape[0]
+    if Xq is not None:
+        _operand(Xq, _I8, (S, K), "Xq", index)
+    if xscale is not None:
+        _operand(xscale, _F32, (S,), "xscale", index)
+
+    def call(st):
+        q = torch.empty((S, K), dtype=_I8, device=X.device) if Xq is None else Xq
+        s = torch.empty(S, dtype=_F32, device=X.device) if xscale is None else xscale
+        rc = load_library().llmint8_quantize_rows(X.data_ptr(), _DTYPES[X.dtype], T, K, at, copies, S, q.data_ptr(),
+                                                  s.data_ptr(), st)
+        if rc:
+            _check(rc, "llmint8_quantize_rows")
+        return q, s
+
+    return _run(index, stream, call)
 
 
 def _product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, stream, where):
-    grouped = offsets is not None
-    nd = 3 if grouped else 2
-    _need(Xq, torch.int8, 2, "Xq")
-    _need(xscale, torch.float32, 1, "xscale")
-    _need(Wq, torch.int8, nd, "Wq")
-    _need(Wscale, torch.float32, nd - 1, "Wscale")
+    index = _first(Xq, (_I8,), 2, "Xq")
+    _first(Wq, (_I8,), 2 if offsets is None else 3, "Wq")
     S, K = Xq.shape
-    N = Wq.shape[-2]
-    lead = tuple(Wq.shape[:-2])
-    _shape(Wq, lead + (N, K), "Wq")
-    _shape(xscale, (S,), "xscale")
-    _shape(Wscale, lead + (N,), "Wscale")
+    shape = tuple(Wq.shape)
+    N, rows = shape[-2], shape[:-1]
+    _operand(Wq, _I8, rows + (K,), "Wq", index)
+    _operand(xscale, _F32, (S,), "xscale", index)
+    _operand(Wscale, _F32, rows, "Wscale", index)
     if bias is not None:
-        _need(bias, torch.float32, nd - 1, "bias")
-        _shape(bias, lead + (N,), "bias")
-    if grouped:
-        _need(offsets, torch.int32, 1, "offsets")
-        _shape(offsets, (lead[0] + 1,), "offsets")
-    if gated and N % 32:
-        raise ValueError(f"a gated product needs N = 2 F with F a multiple of 16, got N = {N}")
-    No = N // 2 if gated else N
+        _operand(bias, _F32, rows, "bias", index)
+    if offsets is not None:
+        _operand(offsets, _I32, (shape[0] + 1,), "offsets", index)
+    No = N
+    if gated:
+        if N % 32:
+            raise ValueError(f"a gated product needs N = 2 F with F a multiple of 16, got N = {N}")
+        No = N // 2
     if Y is not None:
         dtype = Y.dtype
     code = _out_dtype(dtype)
-    _same_device(Xq, xscale=xscale, offsets=offsets, Wq=Wq, Wscale=Wscale, bias=bias, Y=Y)
-    with _On(Xq.device, stream) as st:
-        if Y is None:
-            Y = torch.empty((S, No), dtype=dtype, device=Xq.device)
-        else:
-            _need(Y, dtype, 2, "Y")
-            _shape(Y, (S, No), "Y")
-        lib = load_library()
+    if Y is not None:
+        _operand(Y, dtype, (S, No), "Y", index)
+
+    def call(st):
+        out = torch.empty((S, No), dtype=dtype, device=Xq.device) if Y is None else Y
         b = None if bias is None else bias.data_ptr()
-        if grouped:
-            rc = lib.llmint8_grouped_matmul(Xq.data_ptr(), xscale.data_ptr(), S, K, offsets.data_ptr(), lead[0],
-                                            Wq.data_ptr(), Wscale.data_ptr(), b, N, int(bool(gated)), Y.data_ptr(),
-                                            code, st)
+        lib = load_library()
+        if offsets is None:
+            rc = lib.llmint8_scaled_matmul(Xq.data_ptr(), xscale.data_ptr(), S, K, Wq.data_ptr(), Wscale.data_ptr(), b,
+                                           N, 1 if gated else 0, out.data_ptr(), code, st)
         else:
-            rc = lib.llmint8_scaled_matmul(Xq.data_ptr(), xscale.data_ptr(), S, K, Wq.data_ptr(), Wscale.data_ptr(),
-                                           b, N, int(bool(gated)), Y.data_ptr(), code, st)
-        _check(rc, where)
-    return Y
+            rc = lib.llmint8_grouped_matmul(Xq.data_ptr(), xscale.data_ptr(), S, K, offsets.data_ptr(), shape[0],
+                                            Wq.data_ptr(), Wscale.data_ptr(), b, N, 1 if gated else 0,
+                                            out.data_ptr(), code, st)
+        if rc:
+            _check(rc, where)
+        return out
+
+    return _run(index, stream, call)
 
 
 def llmint8_scaled_matmul(Xq: torch.Tensor, xscale: torch.Tensor, Wq: torch.Tensor, Wscale: torch.Tensor,
@@ -180,23 +181,26 @@ def llmint8_expert_positions(ids: torch.Tensor, experts: int, positions: torch.T
     (positions int32 [T, k], offsets int32 [experts + 1]): expert e's rows are
     offsets[e] .. offsets[e + 1] - 1, stable in the order of ids; a choice
     outside [0, experts) has position -1."""
-    if isinstance(ids, torch.Tensor) and ids.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
-    _need(ids, ids.dtype if isinstance(ids, torch.Tensor) else None, 2, "ids")
+    index = _first(ids, (_I32, torch.int64), 2, "ids")
     T, k = ids.shape
     experts = int(experts)
-    with _On(ids.device, stream) as st:
-        positions = torch.empty((T, k), dtype=torch.int32, device=ids.device) if positions is None else positions
-        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device) if offsets is None else offsets
-        _need(positions, torch.int32, 2, "positions")
-        _need(offsets, torch.int32, 1, "offsets")
-        _shape(positions, (T, k), "positions")
-        _shape(offsets, (experts + 1,), "offsets")
-        _same_device(ids, positions=positions, offsets=offsets)
-        _check(load_library().llmint8_expert_positions(
-            ids.data_ptr(), ids.element_size(), T, k, experts, positions.data_ptr(), offsets.data_ptr(), st),
-            "llmint8_expert_positions")
-    return positions, offsets
+    if experts < 1 or experts > MAX_EXPERTS:
+        raise ValueError(f"experts must be in [1, {MAX_EXPERTS}], got {experts}")
+    if positions is not None:
+        _operand(positions, _I32, (T, k), "positions", index)
+    if offsets is not None:
+        _operand(offsets, _I32, (experts + 1,), "offsets", index)
+
+    def call(st):
+        p = torch.empty((T, k), dtype=_I32, device=ids.device) if positions is None else positions
+        o = torch.empty(experts + 1, dtype=_I32, device=ids.device) if offsets is None else offsets
+        rc = load_library().llmint8_expert_positions(ids.data_ptr(), ids.element_size(), T, k, experts, p.data_ptr(),
+                                                     o.data_ptr(), st)
+        if rc:
+            _check(rc, "llmint8_expert_positions")
+        return p, o
+
+    return _run(index, stream, call)
 
 
 def llmint8_expert_combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor, dtype=None,
@@ -204,22 +208,23 @@ def llmint8_expert_combine(Y: torch.Tensor, positions: torch.Tensor, weights: to
     """out [T, N]: out[t] = sum_j weights[t, j] Y[positions[t, j]] over the
     positions >= 0 (Y [S, N], positions int32 [T, k], weights float32 [T, k]),
     in `dtype` (Y's by default, or out's)."""
-    _float(Y, 2, "Y")
-    _need(positions, torch.int32, 2, "positions")
-    _need(weights, torch.float32, 2, "weights")
+    index = _first(Y, None, 2, "Y")
+    _first(positions, (_I32,), 2, "positions")
     S, N = Y.shape
     T, k = positions.shape
-    _shape(weights, (T, k), "weights")
+    _operand(positions, _I32, (T, k), "positions", index)
+    _operand(weights, _F32, (T, k), "weights", index)
     dtype = out.dtype if out is not None else Y.dtype if dtype is None else dtype
     code = _out_dtype(dtype)
-    _same_device(Y, positions=positions, weights=weights, out=out)
-    with _On(Y.device, stream) as st:
-        if out is None:
-            out = torch.empty((T, N), dtype=dtype, device=Y.device)
-        else:
-            _need(out, dtype, 2, "out")
-            _shape(out, (T, N), "out")
-        _check(load_library().llmint8_expert_combine(
-            Y.data_ptr(), _DTYPES[Y.dtype], S, N, positions.data_ptr(), weights.data_ptr(), T, k, out.data_ptr(),
-            code, st), "llmint8_expert_combine")
-    return out
+    if out is not None:
+        _operand(out, dtype, (T, N), "out", index)
+
+    def call(st):
+        o = torch.empty((T, N), dtype=dtype, device=Y.device) if out is None else out
+        rc = load_library().llmint8_expert_combine(Y.data_ptr(), _DTYPES[Y.dtype], S, N, positions.data_ptr(),
+                                                   weights.data_ptr(), T, k, o.data_ptr(), code, st)
+        if rc:
+            _check(rc, "llmint8_expert_combine")
+        return o
+
+    return _run(index, stream, call)

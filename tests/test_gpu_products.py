@@ -538,8 +538,9 @@ def test_refusals(L):
                  lambda: L.llmint8_expert_combine(X, pos.long(), torch.ones(8, 1, device="cuda"))):
         with pytest.raises((TypeError, ValueError)):
             call()
-    with pytest.raises(L.LLMInt8Error):
-        L.llmint8_expert_positions(pos, L.MAX_EXPERTS + 1)
+    for experts in (0, L.MAX_EXPERTS + 1):
+        with pytest.raises(ValueError):
+            L.llmint8_expert_positions(pos, experts)
     torch.cuda.synchronize()
 
 
