@@ -707,7 +707,7 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   if (rc != LLMINT8_OK) return rc;
   const ProductPlan plan = plan_product(static_cast<int>(S), static_cast<int>(N), static_cast<int>(K),
                                         static_cast<int>(E), grouped, gated != 0, num_sms, max_pairs);
-  if (plan.tiles > INT32_MAX) return LLMINT8_ERR_INVALID_ARG;
+  if (plan.tiles > INT32_MAX - 4096) return LLMINT8_ERR_INVALID_ARG;
   product::Params p;
   p.S = static_cast<int>(S);
   p.N = static_cast<int>(N);
@@ -722,6 +722,8 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   p.H = plan.H;
   p.nN = plan.nN;
   p.BT = plan.BT;
+  p.mt = grouped ? 0 : product::token_tiles(p.S, plan.BT);
+  p.per = product::tile_rows(p.S, p.mt);
   p.quarter = plan.quarter;
   p.b_rows = plan.b_rows;
   p.stages = plan.stages;
@@ -741,9 +743,14 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   bool ok = gated ? encode_tiled<5>(&tw, Wq, {k0, 16, 2 * Eu, Nu / 32, k1}, {Ku, Nu / 2 * Ku, 16 * Ku, product::BK},
                                     {product::BK, 16, 2, H / 32, kpb})
                   : encode_tiled<4>(&tw, Wq, {k0, Nu, k1, Eu}, {Ku, product::BK, Nu * Ku}, {product::BK, H, kpb, 1});
+  // One group that is one tile needs one height of the token copies.
+  const int least = !grouped && S <= p.BT ? p.b_rows / p.quarter - 1 : 0;
   for (int i = 0; ok && i < 4; ++i)
-    ok = encode_tiled<3>(&tx.m[i], Xq, {k0, static_cast<cuuint64_t>(S), k1}, {Ku, product::BK},
-                         {product::BK, static_cast<cuuint32_t>(std::min((i + 1) * p.quarter, p.b_rows)), kpb});
+    if (i >= least && i * p.quarter < p.b_rows)
+      ok = encode_tiled<3>(&tx.m[i], Xq, {k0, static_cast<cuuint64_t>(S), k1}, {Ku, product::BK},
+                           {product::BK, static_cast<cuuint32_t>((i + 1) * p.quarter), kpb});
+  for (int i = 0; i < 4; ++i)
+    if (i < least || i * p.quarter >= p.b_rows) tx.m[i] = tx.m[least];
   if (!ok) return LLMINT8_ERR_CUDA;
   const ProductKernel kern = plan.pair ? (gated ? product_kernel_for<true, true>(dtype) : product_kernel_for<true, false>(dtype))
                                        : (gated ? product_kernel_for<false, true>(dtype) : product_kernel_for<false, false>(dtype));

@@ -21,7 +21,7 @@
 // unit, + units, ...; tile w belongs to the group whose cumulative tile count covers it, found in
 // shared memory from the device's offsets (the host never waits for them).
 // Warp 0 copies (TMA, 128-byte swizzle), warp 1 issues tcgen05.mma kind::i8
-// and owns TMEM, warps 2-9 write the results.  Two 256-column accumulators
+// and owns TMEM, warps 2-17 write the results.  Two 256-column accumulators
 // let the next tile's products run while the epilogue drains the last one.
 // Every mbarrier wait is bounded.
 #pragma once
@@ -38,18 +38,18 @@ constexpr int MAX_BT = 256;        // most tokens of a tile (MMA N)
 constexpr int KPB_MAX = 4;         // k-blocks per stage
 constexpr int MAX_STAGES = 12;
 constexpr int MAX_GROUPS = 1024;
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 512;     // two accumulators of MAX_BT columns
 constexpr int RING_BYTES = 192 * 1024;  // stages, and 16 KiB past the last one (see SLACK)
 // Behind the ring: the epilogue's staging.  A tile of fewer than 128 weight
 // rows is multiplied as 128, and the lanes past its end (never stored) read
 // whatever follows in shared memory: after the last stage, these 16 KiB.
-constexpr int STAGING_BYTES = 8 * 1024;       // of one set of 4 epilogue warps
-constexpr int SLACK_BYTES = 2 * STAGING_BYTES;
+constexpr int STAGING_BYTES = 1024;  // of one epilogue warp
+constexpr int SLACK_BYTES = EPI_WARPS * STAGING_BYTES;
 static_assert(SLACK_BYTES >= BM * BK, "the last stage's 128 rows end inside shared memory");
 constexpr int SX_BYTES = 2 * MAX_BT * 4;
-constexpr int GROUP_BYTES = 2 * (MAX_GROUPS + 1) * 4;
+constexpr int GROUP_BYTES = 2 * (MAX_GROUPS + 1) * 4 + MAX_GROUPS * 4 + MAX_GROUPS * 2;
 constexpr int BAR_BYTES = 512;
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + SLACK_BYTES + SX_BYTES + GROUP_BYTES + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -66,6 +66,7 @@ struct Params {
   int H;               // weight rows of a tile and CTA (a multiple of 8; of 32 when gated)
   int nN;              // tiles along the channels (2 H rows each for CTA pairs)
   int BT;              // most tokens of a tile, a multiple of 16
+  int mt, per;         // without offsets: token tiles, rows of each
   int quarter;         // token rows of a copy come in 1..4 quarters (a multiple of 8 rows each)
   int b_rows;          // token rows that a k-block of a stage has room for
   int stages;
@@ -83,49 +84,99 @@ struct TokenMaps {
   CUtensorMap m[4];
 };
 
-// A tile: `tok` tokens from row m0 of Xq / Y, weight rows (or gated channel
-// pairs) from tile nt of group e.
-struct Tile {
-  int e, m0, tok, nt;
+// A group's rows are cut into mt tiles of `per` rows (a multiple of 16; the
+// last may be shorter).
+__host__ __device__ inline int token_tiles(int m, int bt) { return (m + bt - 1) / bt; }
+__host__ __device__ inline int tile_rows(int m, int mt) { return mt ? ((m + mt - 1) / mt + 15) / 16 * 16 : 0; }
+
+// The groups, in shared memory.
+struct Groups {
+  int* off;        // [E + 1] rows
+  int* cum;        // [E + 1] tiles before the group
+  int* mt;         // [E]
+  uint16_t* per;   // [E]
 };
 
-// Tiles of a group of m rows along its tokens, and rows of each (a multiple of
-// 16, so that the group's tiles are equal but for the last).
-__device__ __forceinline__ int token_tiles(int m, int bt) { return (m + bt - 1) / bt; }
-
-__device__ __forceinline__ Tile find_tile(const Params& p, const int* off, const int* cum, int w) {
-  int lo = 0, hi = p.E;  // cum[lo] <= w < cum[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] <= w)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int begin = off[lo], m = off[lo + 1] - begin;
-  const int mt = token_tiles(m, p.BT);
-  const int per = ((m + mt - 1) / mt + 15) / 16 * 16;
-  const int r = w - cum[lo];
-  Tile t;
-  t.e = lo;
-  t.nt = r / mt;
-  const int i = r - t.nt * mt;
-  t.m0 = begin + i * per;
-  t.tok = min(per, m - i * per);
-  return t;
+// a / b for 0 <= a < 2^20, b >= 1: (a + 1/2) / b is at least 1 / (2 b) away
+// from every integer, and the two approximate steps are off by less than
+// (a + 1) / b * 2^-21.
+__device__ __forceinline__ int small_div(int a, int b) {
+  return __float2int_rz(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b)));
 }
 
-// The groups' bounds and cumulative tile counts, by one warp.  Bounds that
-// fall outside [0, S] or run backwards are clamped (no row outside Xq or Y is
-// touched) and recorded in the error word.
-__device__ __forceinline__ void scan_groups(const Params& p, int* off, int* cum) {
+// The tiles w = unit, unit + units, ... of a CTA (pair).  Within a group the
+// token tiles of one weight tile come one after the other (the weights are
+// then read from L2); moving on needs no division of large numbers: only the
+// step `units` and the rest below it are divided.
+struct Walk {
+  int w, total, units;
+  int g, r, mt, nt, i;     // group, tile within it, its token tiles; r = nt * mt + i
+  int dq, dr;              // units / mt, units % mt
+  int begin, rows, per, tiles;
+
+  __device__ void enter(const Groups& s, int group) {
+    g = group;
+    begin = s.off[g];
+    rows = s.off[g + 1] - begin;
+    mt = s.mt[g];
+    per = s.per[g];
+    tiles = s.cum[g + 1] - s.cum[g];
+    r = w - s.cum[g];
+    nt = small_div(r, mt);
+    i = r - nt * mt;
+    dq = small_div(units, mt);
+    dr = units - dq * mt;
+  }
+  // The group whose tiles hold w, from group `lo` on.
+  __device__ void search(const Params& p, const Groups& s, int lo) {
+    int hi = p.E;  // cum[lo] <= w < cum[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.cum[mid] <= w)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    enter(s, lo);
+  }
+  __device__ Walk(const Params& p, const Groups& s, int unit, int step) {
+    w = unit;
+    units = step;
+    total = s.cum[p.E];
+    if (w < total) search(p, s, 0);
+  }
+  __device__ bool more() const { return w < total; }
+  __device__ void next(const Params& p, const Groups& s) {
+    w += units;
+    r += units;
+    if (r < tiles) {
+      nt += dq;
+      i += dr;
+      if (i >= mt) {
+        i -= mt;
+        ++nt;
+      }
+    } else if (w < total) {
+      search(p, s, g + 1);
+    }
+  }
+  __device__ int row() const { return begin + i * per; }                  // first row of Xq / Y
+  __device__ int tokens() const { return min(per, rows - i * per); }
+};
+
+// Fills the groups' tables, by one warp.  Bounds that fall outside [0, S] or
+// run backwards are clamped (no row outside Xq or Y is touched) and recorded
+// in the error word.
+__device__ __forceinline__ void scan_groups(const Params& p, const Groups& s) {
   const int lane = static_cast<int>(lane_id());
   if (!p.offsets) {
     if (lane == 0) {
-      off[0] = 0;
-      off[1] = p.S;
-      cum[0] = 0;
-      cum[1] = token_tiles(p.S, p.BT) * p.nN;
+      s.off[0] = 0;
+      s.off[1] = p.S;
+      s.cum[0] = 0;
+      s.cum[1] = p.mt * p.nN;
+      s.mt[0] = p.mt;
+      s.per[0] = static_cast<uint16_t>(p.per);
     }
     return;
   }
@@ -135,8 +186,8 @@ __device__ __forceinline__ void scan_groups(const Params& p, int* off, int* cum)
     const int o = p.offsets[0];
     prev = min(max(o, 0), p.S);
     bad = prev != o;
-    off[0] = prev;
-    cum[0] = 0;
+    s.off[0] = prev;
+    s.cum[0] = 0;
   }
   prev = __shfl_sync(0xffffffffu, prev, 0);
   for (int g0 = 0; g0 < p.E; g0 += 32) {
@@ -153,15 +204,18 @@ __device__ __forceinline__ void scan_groups(const Params& p, int* off, int* cum)
     bad |= g < p.E && end != o;
     int begin = __shfl_up_sync(0xffffffffu, end, 1);
     if (lane == 0) begin = prev;
-    int n = g < p.E ? token_tiles(end - begin, p.BT) * p.nN : 0;
+    const int mt = token_tiles(end - begin, p.BT);
+    int n = g < p.E ? mt * p.nN : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, n, d);
       if (lane >= d) n += v;
     }
     if (g < p.E) {
-      off[g + 1] = end;
-      cum[g + 1] = base + n;
+      s.off[g + 1] = end;
+      s.cum[g + 1] = base + n;
+      s.mt[g] = mt;
+      s.per[g] = static_cast<uint16_t>(tile_rows(end - begin, mt));
     }
     base += __shfl_sync(0xffffffffu, n, 31);
     prev = __shfl_sync(0xffffffffu, end, 31);
@@ -196,37 +250,36 @@ __device__ __forceinline__ uint32_t pack_two(float a, float b) {
 
 // ------------------------------------------------------------ epilogue
 // The accumulator has channels along the TMEM lanes and tokens along the
-// columns; Y has channels along its rows.  A set of 4 warps turns CHUNK tokens
-// by all channels of the tile around through shared memory, so that Y is
-// written 16 bytes a thread in whole runs of the tile's channels.  (Storing
-// each lane's channel directly, 64 bytes per warp and token, took 9.7 us per
-// tile of 128 x 256 against 3.3 us of products at K = 1408.)
+// columns; Y has channels along its rows.  A warp turns CHUNK tokens by the
+// channels of its 32 lanes around through its own 1 KiB of shared memory, so
+// that Y is written 16 bytes a thread, 32 to 128 bytes of a row at a time, and
+// no warp waits for another.
 //
 // tcgen05.ld 16x256b gives a thread two tokens of one channel per register
 // pair: the shape that stmatrix.trans stores 8 channels of a token from.  In
 // a gated tile TMEM lanes 0-15 of a quadrant hold the gates and lanes 16-31 the
 // values of the same 16 channels, so both halves of an output meet in a thread.
-//
-// Staging layout: [token][channel], the 16-byte (16-bit types: chunk index ^
-// token % 8; binary32: word index ^ 8 (token / 2 % 4)) position swizzled so
-// that neither the writes nor the reads meet in a bank.
 template <bool GATED, int OT>
 struct Epilogue {
   static constexpr bool k32 = OT == kF32;
-  static constexpr int CH = GATED ? BM / 2 : BM;             // channels of a CTA's tile
-  static constexpr int ROW_BYTES = CH * (k32 ? 4 : 2);
-  static constexpr int CHUNK = k32 && !GATED ? 16 : 32;      // tokens staged at a time
-  static constexpr int VEC = k32 ? 4 : 8;                    // elements in 16 bytes
-  static_assert(CHUNK * ROW_BYTES <= STAGING_BYTES, "staging");
+  static constexpr int SIZE = k32 ? 4 : 2;
+  static constexpr int CH = GATED ? 16 : 32;                 // channels of a warp
+  static constexpr int CHUNK = STAGING_BYTES / (CH * SIZE);  // tokens staged at a time: 8, 16 or 32
+  static constexpr int VEC = 16 / SIZE;                      // elements in 16 bytes
 
-  __device__ static uint32_t at(int token, int channel) {    // byte offset in the staging
-    if constexpr (k32) return token * ROW_BYTES + ((channel ^ (((token >> 1) & 3) << 3)) << 2);
-    const int chunk = (channel >> 3) ^ (token & 7);
-    return token * ROW_BYTES + (chunk << 4) + ((channel & 7) << 1);
+  // Byte offset of a token's channel in the staging, [token][channel] with the
+  // 16-byte pieces (binary32: pairs of pieces) of each 128 bytes permuted so
+  // that neither the writes nor the reads meet in a bank.
+  __device__ static uint32_t at(int token, int channel) {
+    const int byte = (token * CH + channel) * SIZE;
+    if constexpr (k32) return byte ^ (((token >> 1) & 3) << 5);
+    if constexpr (!k32 && !GATED) return byte ^ (((token >> 1) & 3) << 4);
+    return byte ^ (((token >> 2) & 1) << 4);
   }
 
-  // Outputs of CHUNK columns, staged by this warp.  `sw`, `b`: of TMEM lanes l / 4 + {0, 8, 16, 24} of the quadrant.
-  __device__ static void stage(uint8_t* st, uint32_t addr, int q, int lane, const float* sx, const float (&sw)[4],
+  // Outputs of CHUNK columns, staged by this warp.  `sw`, `b`: of TMEM lanes
+  // l / 4 + {0, 8, 16, 24} of the quadrant.
+  __device__ static void stage(uint8_t* st, uint32_t addr, int lane, const float* sx, const float (&sw)[4],
                                const float (&b)[4]) {
     uint32_t lo[CHUNK / 2], hi[CHUNK / 2];  // TMEM lanes 0-15 and 16-31
     [[maybe_unused]] uint32_t keep0 = 0, keep1 = 0;
@@ -236,6 +289,7 @@ struct Epilogue {
     tmem_regs_ready(lo);
     tmem_regs_ready(hi);
     const int r = lane >> 2, col = 2 * (lane & 3);
+    const int m = lane >> 3, j = lane & 7;  // stmatrix: matrix and token of this lane's address
     auto z = [](uint32_t acc, float sxv, float swv, float bv) {
       return static_cast<float>(static_cast<int32_t>(acc)) * sxv * swv + bv;
     };
@@ -258,53 +312,48 @@ struct Epilogue {
           y[3][h] = z3;
         }
       }
-      constexpr int NB = GATED ? 2 : 4;  // channel blocks of this warp
       if constexpr (k32) {
 #pragma unroll
-        for (int c = 0; c < NB; ++c)
+        for (int c = 0; c < CH / 8; ++c)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float*>(st + at(8 * i + col + h, (q * NB + c) * 8 + r)) = y[c][h];
+            *reinterpret_cast<float*>(st + at(8 * i + col + h, c * 8 + r)) = y[c][h];
       } else if constexpr (GATED) {
-        // two channel blocks of 8 tokens: the second pair of matrices is the
-        // next 8 tokens', held back until they are there
+        // two channel blocks of 8 tokens; the other two matrices are the next
+        // 8 tokens', so these wait for them
         if (i & 1) {
-          const int m = lane >> 3, j = lane & 7;  // matrix and token of this lane's address
-          stmatrix_x4_trans(smem_addr(st) + at(8 * (i - 1 + (m >> 1)) + j, (q * 2 + (m & 1)) * 8), keep0, keep1,
+          stmatrix_x4_trans(smem_addr(st) + at(8 * (i - 1 + (m >> 1)) + j, (m & 1) * 8), keep0, keep1,
                             pack_two<OT>(y[0][0], y[0][1]), pack_two<OT>(y[1][0], y[1][1]));
         } else {
           keep0 = pack_two<OT>(y[0][0], y[0][1]);
           keep1 = pack_two<OT>(y[1][0], y[1][1]);
         }
       } else {
-        const int m = lane >> 3, j = lane & 7;
-        stmatrix_x4_trans(smem_addr(st) + at(8 * i + j, (q * 4 + m) * 8), pack_two<OT>(y[0][0], y[0][1]),
+        stmatrix_x4_trans(smem_addr(st) + at(8 * i + j, m * 8), pack_two<OT>(y[0][0], y[0][1]),
                           pack_two<OT>(y[1][0], y[1][1]), pack_two<OT>(y[2][0], y[2][1]),
                           pack_two<OT>(y[3][0], y[3][1]));
       }
     }
   }
 
-  // The staged tokens to Y rows m .., channels c .. c + n - 1 (n <= CH), by
-  // the 128 threads of the set.
-  __device__ static void write(const uint8_t* st, void* Y, int No, int64_t m, int cnt, int c, int n, int tid) {
-    constexpr int PER_ROW = CH / VEC, ROWS = 128 / PER_ROW;
-    constexpr int SIZE = k32 ? 4 : 2;
+  // The staged tokens (the first cnt) to Y from row m on, channels c .. c + n - 1.
+  __device__ static void write(const uint8_t* st, void* Y, int No, int64_t m, int cnt, int c, int n, int lane) {
+    constexpr int PER_ROW = CH / VEC, ROWS = 32 / PER_ROW;
     uint8_t* y = static_cast<uint8_t*>(Y);
     if (No % VEC == 0) {  // n is a multiple of VEC too
-      const int v = (tid % PER_ROW) * VEC;
+      const int v = (lane % PER_ROW) * VEC;
       if (v < n) {
 #pragma unroll
         for (int t0 = 0; t0 < CHUNK; t0 += ROWS) {
-          const int t = t0 + tid / PER_ROW;
+          const int t = t0 + lane / PER_ROW;
           if (t < cnt)
             *reinterpret_cast<uint4*>(y + ((m + t) * No + c + v) * SIZE) =
                 *reinterpret_cast<const uint4*>(st + at(t, v));
         }
       }
     } else {
-      for (int i = tid; i < cnt * CH; i += 128) {
-        const int t = i / CH, v = i % CH;
+      const int v = lane % CH;
+      for (int t = lane / CH; t < cnt; t += 32 / CH) {
         if (v < n) {
           if constexpr (k32)
             reinterpret_cast<float*>(y)[(m + t) * No + c + v] = *reinterpret_cast<const float*>(st + at(t, v));
@@ -315,6 +364,11 @@ struct Epilogue {
     }
   }
 };
+
+// Quarters that hold `rows` token rows (1..4).
+__device__ __forceinline__ int quarters_of(const Params& p, int rows) {
+  return 1 + (rows > p.quarter) + (rows > 2 * p.quarter) + (rows > 3 * p.quarter);
+}
 
 // GATED: the weight copies interleave 16 gate rows with the 16 value rows of
 // the same channels, so that lanes l and l + 16 of a warp hold the two halves
@@ -333,8 +387,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* sx_s = reinterpret_cast<float*>(smem + RING_BYTES + SLACK_BYTES);  // [2][MAX_BT]
-  int* off = reinterpret_cast<int*>(sx_s + 2 * MAX_BT);                     // [E + 1]
-  int* cum = off + MAX_GROUPS + 1;                                          // [E + 1]
+  Groups groups;
+  groups.off = reinterpret_cast<int*>(sx_s + 2 * MAX_BT);
+  groups.cum = groups.off + MAX_GROUPS + 1;
+  groups.mt = groups.cum + MAX_GROUPS + 1;
+  groups.per = reinterpret_cast<uint16_t*>(groups.mt + MAX_GROUPS);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SMEM_BYTES - 1024 - BAR_BYTES);
   uint64_t* empty = full + MAX_STAGES;
   uint64_t* tfull = empty + MAX_STAGES;  // [2]
@@ -372,22 +429,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_relinquish();
     }
   }
+  tc_fence_before();
+  __syncwarp();
+  if constexpr (PAIR)
+    cluster_sync();  // both CTAs' barriers are initialised before a copy or commit reaches them
   // The codes, scales and offsets may come from the kernel before this one,
   // and so may the weights (a user may have quantised them just now): nothing
   // is read before that kernel is done.  Only then may the next one start, so
   // that a kernel two calls later never runs beside one two calls earlier.
   pdl_wait();
   pdl_launch_dependents();
-  if (warp == 2) scan_groups(p, off, cum);
-  tc_fence_before();
-  __syncwarp();
-  if constexpr (PAIR)
-    cluster_sync();  // both CTAs' barriers are initialised before a copy or commit reaches them
-  else
-    __syncthreads();
+  if (warp == 2) scan_groups(p, groups);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = cum[p.E];
   const int a_bytes = p.H * BK;                     // of one k-block
   const int b_bytes = p.b_rows * BK;
   const int stage_bytes = (a_bytes + b_bytes) * p.KPB;
@@ -403,12 +458,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     int it = 0, s = 0;      // stages filled so far; the stage to fill next
     uint32_t phase = 1;     // parity its `empty` barrier had before this round (passes at once in round 0)
     bool ok = true;
-    for (int w = unit; ok && w < total; w += units) {
-      const Tile t = find_tile(p, off, cum, w);
-      const int cols = (t.tok + 15) / 16 * 16;     // MMA N
-      const int mine = PAIR ? cols / 2 : cols;     // token rows this CTA copies
-      const int x0 = t.m0 + rank * mine;
-      const int quarters = (mine + p.quarter - 1) / p.quarter;
+    for (Walk t(p, groups, unit, units); ok && t.more(); t.next(p, groups)) {
+      const int cols = (t.tokens() + 15) / 16 * 16;  // MMA N
+      const int mine = PAIR ? cols / 2 : cols;       // token rows this CTA copies
+      const int x0 = t.row() + rank * mine;
+      const int quarters = quarters_of(p, mine);
       const CUtensorMap* tmap_x = &tmaps_x.m[quarters - 1];
       const int wt = PAIR ? 2 * t.nt + rank : t.nt;  // this CTA's weight rows, in units of H
       const uint32_t tx = static_cast<uint32_t>((PAIR ? 2 : 1) * p.KPB * (a_bytes + quarters * p.quarter * BK));
@@ -421,16 +475,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t bar = map_shared_rank(&full[s], 0);
             if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
             if constexpr (GATED)
-              tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.e, wt * (p.H / 32), kb);
+              tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.g, wt * (p.H / 32), kb);
             else
-              tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.e);
+              tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.g);
             tma_load_3d_pair(stage_b(s), tmap_x, bar, x, x0, kb);
           } else {
             mbar_arrive_expect_tx(&full[s], tx);
             if constexpr (GATED)
-              tma_load_5d(stage_a(s), &tmap_w, &full[s], x, 0, 2 * t.e, wt * (p.H / 32), kb);
+              tma_load_5d(stage_a(s), &tmap_w, &full[s], x, 0, 2 * t.g, wt * (p.H / 32), kb);
             else
-              tma_load_4d(stage_a(s), &tmap_w, &full[s], x, wt * p.H, kb, t.e);
+              tma_load_4d(stage_a(s), &tmap_w, &full[s], x, wt * p.H, kb, t.g);
             tma_load_3d(stage_b(s), tmap_x, &full[s], x, x0, kb);
           }
         }
@@ -459,13 +513,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       int s = 0, tc = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int w = unit; ok && w < total; w += units, ++tc) {
-        const Tile t = find_tile(p, off, cum, w);
-        const int cols = (t.tok + 15) / 16 * 16;
+      for (Walk t(p, groups, unit, units); ok && t.more(); t.next(p, groups), ++tc) {
+        const int cols = (t.tokens() + 15) / 16 * 16;
         const uint32_t idesc = idesc_i8_s32(PAIR ? 2 * BM : BM, cols);
         // k-blocks of a stage lie as the copy put them: its rows apart
-        const uint32_t b_step =
-            static_cast<uint32_t>(((PAIR ? cols / 2 : cols) + p.quarter - 1) / p.quarter * p.quarter * BK) >> 4;
+        const uint32_t b_step = static_cast<uint32_t>(quarters_of(p, PAIR ? cols / 2 : cols) * p.quarter * BK) >> 4;
         const int buf = tc & 1;
         if (tc >= 2) {
           ok = mbar_wait_stage<PAIR>(&tempty[buf], ((tc >> 1) - 1) & 1, p.wait_ns, kErrTimeoutMma);
@@ -516,51 +568,68 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ epilogue
     using Epi = Epilogue<GATED, OT>;
     const int q = warp & 3;                   // TMEM lane quadrant of this warp
-    const int set = (warp - 2) >> 2;          // two sets of 4 warps share the columns
+    const int set = (warp - 2) >> 2;          // sets of 4 warps take turns at the columns
     const int etid = static_cast<int>(threadIdx.x) - 64;
-    const int stid = etid & 127;
-    const uint32_t set_bar = 2u + static_cast<uint32_t>(set);
-    uint8_t* staging = smem + RING_BYTES + set * STAGING_BYTES;
+    uint8_t* staging = smem + RING_BYTES + (warp - 2) * STAGING_BYTES;
     const int tile_ch = GATED ? p.H / 2 : p.H;  // channels of this CTA's tile
+    // What a tile's outputs need from global memory, fetched while the tile
+    // before it is written: a token's scale (one thread each) and this lane's
+    // channel scales and biases.  (Fetched at its own turn, it made 3400 cycles
+    // between two tiles.)
+    struct Ahead {
+      int m0, tok, c, n;  // rows of Y; this warp's channels: n from c on inside Y and the tile
+      float sx, sw[4], b[4];
+    };
+    auto fetch = [&](const Walk& t) {
+      Ahead a;
+      a.m0 = t.row();
+      a.tok = t.tokens();
+      a.c = (PAIR ? 2 * t.nt + rank : t.nt) * tile_ch + q * Epi::CH;
+      a.n = min(min(tile_ch - q * Epi::CH, Epi::CH), p.No - a.c);
+      a.sx = etid < a.tok ? p.sx[a.m0 + etid] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // TMEM lanes l / 4 + 8 i of the quadrant
+        const int ch = (lane >> 2) + 8 * (GATED ? i & 1 : i);
+        const int64_t at = static_cast<int64_t>(t.g) * p.N + a.c + ch + (GATED && i >= 2 ? p.No : 0);
+        a.sw[i] = ch < a.n ? p.sw[at] : 0.0f;
+        a.b[i] = ch < a.n && p.bias ? p.bias[at] : 0.0f;
+      }
+      return a;
+    };
+    static_assert(32 * EPI_WARPS >= MAX_BT, "a thread for each token's scale");
     int tc = 0;
-    for (int w = unit; w < total; w += units, ++tc) {
-      const Tile t = find_tile(p, off, cum, w);
+    Walk t(p, groups, unit, units);
+    Ahead next;
+    if (t.more()) next = fetch(t);
+    for (; t.more(); ++tc) {
+      const Ahead a = next;
       const int buf = tc & 1;
       float* sxb = sx_s + buf * MAX_BT;
       // The buffer's readers two tiles ago are past the previous tile's barrier.
-      for (int j = etid; j < t.tok; j += 32 * EPI_WARPS) sxb[j] = p.sx[t.m0 + j];
-      const int c = (PAIR ? 2 * t.nt + rank : t.nt) * tile_ch;  // first channel
-      const int n = min(tile_ch, p.No - c);                     // channels inside Y (<= 0: none)
-      float sw[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // TMEM lanes l / 4 + 8 i of the quadrant
-        const int ch = GATED ? q * 16 + (lane >> 2) + 8 * (i & 1) : q * 32 + (lane >> 2) + 8 * i;
-        const int64_t at = static_cast<int64_t>(t.e) * p.N + c + ch + (GATED && i >= 2 ? p.No : 0);
-        sw[i] = ch < n ? p.sw[at] : 0.0f;
-        b[i] = ch < n && p.bias ? p.bias[at] : 0.0f;
-      }
+      if (etid < a.tok) sxb[etid] = a.sx;
       // One thread polls, the others sleep at the barrier.
       const bool ok = etid != 0 || mbar_wait_stage(&tfull[buf], (tc >> 1) & 1, p.wait_ns, kErrTimeoutEpilogue);
       if (!named_barrier_and(1, 32 * EPI_WARPS, ok)) break;  // also: sxb is written
       tc_fence_after();
+      t.next(p, groups);
+      if (t.more()) next = fetch(t);
       const uint32_t addr =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * MAX_BT);
-      if (n > 0) {
-        for (int c0 = set * Epi::CHUNK; c0 < t.tok; c0 += 2 * Epi::CHUNK) {
-          if (c0 >= 2 * Epi::CHUNK) named_barrier(set_bar, 128);  // the staging has been read
-          Epi::stage(staging, addr + c0, q, lane, sxb + c0, sw, b);
-          named_barrier(set_bar, 128);
-          Epi::write(staging, p.Y, p.No, t.m0 + c0, min(Epi::CHUNK, t.tok - c0), c, n, stid);
+      if (a.n > 0) {
+        for (int c0 = set * Epi::CHUNK; c0 < a.tok; c0 += EPI_WARPS / 4 * Epi::CHUNK) {
+          Epi::stage(staging, addr + c0, lane, sxb + c0, a.sw, a.b);
+          __syncwarp();
+          Epi::write(staging, p.Y, p.No, a.m0 + c0, min(Epi::CHUNK, a.tok - c0), a.c, a.n, lane);
+          __syncwarp();
         }
       }
       // This warp has read its columns: the MMAs of the tile after next may
-      // write them.  (The next tile's barrier keeps the staging until all of
-      // the set has read it.)
+      // write them.
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if constexpr (PAIR)
-          mbar_arrive_cluster(map_shared_rank(&tempty[buf], 0));
+          mbar_arrive_remote(map_shared_rank(&tempty[buf], 0));
         else
           mbar_arrive(&tempty[buf]);
       }

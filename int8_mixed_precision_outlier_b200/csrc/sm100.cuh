@@ -582,6 +582,14 @@ __device__ __forceinline__ void tmem_ld_16lanes(uint32_t taddr, uint32_t (&r)[8]
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld_16lanes(uint32_t taddr, uint32_t (&r)[4]) {  // 8 columns
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_regs_ready(uint32_t (&r)[4]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]));
+}
 __device__ __forceinline__ void tmem_regs_ready(uint32_t (&r)[8]) {
   asm volatile(""
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
@@ -660,6 +668,13 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // Arrive once on an mbarrier of any CTA of the cluster (shared::cluster address).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+// The same with a release that orders this CTA's accesses only, for handing
+// over tensor memory: a release at cluster scope would wait until this
+// thread's global stores have reached L2 (about 2000 cycles per tile of the
+// product kernel's epilogue).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 // Every thread of every CTA of the cluster: a hardware barrier (all CTAs of a
 // cluster are resident together), with release/acquire of shared memory.

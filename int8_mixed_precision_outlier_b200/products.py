@@ -21,6 +21,7 @@ MAX_EXPERTS = 1024
 
 _Tensor = torch.Tensor
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the pointer alone: 3 us less than a Stream object
+_current_device = torch.cuda.current_device
 
 
 def _refuse(t, dtype, shape, name, index):
@@ -60,7 +61,7 @@ def _run(index: int, stream, call):
     """call(pointer of the stream) with the tensors' device and the call's
     stream current, so that an output belongs to the stream that writes it."""
     if stream is None:
-        if index == torch.cuda.current_device():
+        if index == _current_device():
             return call(_raw_stream(index))
         with torch.cuda.device(index):
             return call(_raw_stream(index))
@@ -100,7 +101,7 @@ def llmint8_quantize_rows(X: torch.Tensor, positions: torch.Tensor | None = None
         _operand(xscale, _F32, (S,), "xscale", index)
 
     def call(st):
-        q = torch.empty((S, K), dtype=_I8, device=X.device) if Xq is None else Xq
+        q = torch.empty(S, K, dtype=_I8, device=X.device) if Xq is None else Xq
         s = torch.empty(S, dtype=_F32, device=X.device) if xscale is None else xscale
         rc = load_library().llmint8_quantize_rows(X.data_ptr(), _DTYPES[X.dtype], T, K, at, copies, S, q.data_ptr(),
                                                   s.data_ptr(), st)
@@ -111,46 +112,75 @@ def llmint8_quantize_rows(X: torch.Tensor, positions: torch.Tensor | None = None
     return _run(index, stream, call)
 
 
-def _product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, stream, where):
+def _check_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y):
+    """Raises for what is wrong with a product's arguments, one by one."""
     index = _first(Xq, (_I8,), 2, "Xq")
     _first(Wq, (_I8,), 2 if offsets is None else 3, "Wq")
     S, K = Xq.shape
-    shape = tuple(Wq.shape)
-    N, rows = shape[-2], shape[:-1]
+    rows = tuple(Wq.shape[:-1])
     _operand(Wq, _I8, rows + (K,), "Wq", index)
     _operand(xscale, _F32, (S,), "xscale", index)
     _operand(Wscale, _F32, rows, "Wscale", index)
     if bias is not None:
         _operand(bias, _F32, rows, "bias", index)
     if offsets is not None:
-        _operand(offsets, _I32, (shape[0] + 1,), "offsets", index)
-    No = N
-    if gated:
-        if N % 32:
-            raise ValueError(f"a gated product needs N = 2 F with F a multiple of 16, got N = {N}")
-        No = N // 2
+        _operand(offsets, _I32, (rows[0] + 1,), "offsets", index)
+    if gated and rows[-1] % 32:
+        raise ValueError(f"a gated product needs N = 2 F with F a multiple of 16, got N = {rows[-1]}")
+    _out_dtype(dtype if Y is None else Y.dtype)
     if Y is not None:
-        dtype = Y.dtype
-    code = _out_dtype(dtype)
-    if Y is not None:
-        _operand(Y, dtype, (S, No), "Y", index)
+        _operand(Y, Y.dtype, (S, rows[-1] // 2 if gated else rows[-1]), "Y", index)
 
-    def call(st):
-        out = torch.empty((S, No), dtype=dtype, device=Xq.device) if Y is None else Y
-        b = None if bias is None else bias.data_ptr()
-        lib = load_library()
-        if offsets is None:
-            rc = lib.llmint8_scaled_matmul(Xq.data_ptr(), xscale.data_ptr(), S, K, Wq.data_ptr(), Wscale.data_ptr(), b,
-                                           N, 1 if gated else 0, out.data_ptr(), code, st)
-        else:
-            rc = lib.llmint8_grouped_matmul(Xq.data_ptr(), xscale.data_ptr(), S, K, offsets.data_ptr(), shape[0],
-                                            Wq.data_ptr(), Wscale.data_ptr(), b, N, 1 if gated else 0,
-                                            out.data_ptr(), code, st)
-        if rc:
-            _check(rc, where)
-        return out
 
-    return _run(index, stream, call)
+def _product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, stream, where):
+    try:
+        S, K = Xq.shape
+        shape = Wq.shape
+        rows = shape[:-1]
+        N = No = rows[-1]
+        if gated:
+            No = N // 2
+        if Y is not None:
+            dtype = Y.dtype
+        index = Xq.get_device()
+        # _check_product in one expression
+        fine = (index >= 0 and shape[-1] == K and Xq.dtype is _I8 and Wq.dtype is _I8 and xscale.dtype is _F32
+                and Wscale.dtype is _F32 and xscale.shape == (S,) and Wscale.shape == rows and Xq.is_contiguous()
+                and Wq.is_contiguous() and xscale.is_contiguous() and Wscale.is_contiguous()
+                and Wq.get_device() == index and xscale.get_device() == index and Wscale.get_device() == index
+                and (len(rows) == 1 if offsets is None else len(rows) == 2 and offsets.dtype is _I32
+                     and offsets.shape == (rows[0] + 1,) and offsets.is_contiguous() and offsets.get_device() == index)
+                and (bias is None or bias.dtype is _F32 and bias.shape == rows and bias.is_contiguous()
+                     and bias.get_device() == index)
+                and (Y is None or Y.shape == (S, No) and Y.is_contiguous() and Y.get_device() == index)
+                and (not gated or N % 32 == 0) and dtype in _DTYPES)
+    except (AttributeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _check_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y)
+    if stream is not None or index != _current_device():
+        return _run(index, stream,
+                    lambda st: _launch_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, st, where))
+    return _launch_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, _raw_stream(index), where)
+
+
+def _launch_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, st, where):
+    S, K = Xq.shape
+    N = Wq.shape[-2]
+    if Y is None:
+        Y = torch.empty(S, N // 2 if gated else N, dtype=dtype, device=Xq.device)
+    b = None if bias is None else bias.data_ptr()
+    lib = load_library()
+    if offsets is None:
+        rc = lib.llmint8_scaled_matmul(Xq.data_ptr(), xscale.data_ptr(), S, K, Wq.data_ptr(), Wscale.data_ptr(), b, N,
+                                       1 if gated else 0, Y.data_ptr(), _DTYPES[dtype], st)
+    else:
+        rc = lib.llmint8_grouped_matmul(Xq.data_ptr(), xscale.data_ptr(), S, K, offsets.data_ptr(), Wq.shape[0],
+                                        Wq.data_ptr(), Wscale.data_ptr(), b, N, 1 if gated else 0, Y.data_ptr(),
+                                        _DTYPES[dtype], st)
+    if rc:
+        _check(rc, where)
+    return Y
 
 
 def llmint8_scaled_matmul(Xq: torch.Tensor, xscale: torch.Tensor, Wq: torch.Tensor, Wscale: torch.Tensor,
@@ -192,7 +222,7 @@ def llmint8_expert_positions(ids: torch.Tensor, experts: int, positions: torch.T
         _operand(offsets, _I32, (experts + 1,), "offsets", index)
 
     def call(st):
-        p = torch.empty((T, k), dtype=_I32, device=ids.device) if positions is None else positions
+        p = torch.empty(T, k, dtype=_I32, device=ids.device) if positions is None else positions
         o = torch.empty(experts + 1, dtype=_I32, device=ids.device) if offsets is None else offsets
         rc = load_library().llmint8_expert_positions(ids.data_ptr(), ids.element_size(), T, k, experts, p.data_ptr(),
                                                      o.data_ptr(), st)
@@ -220,7 +250,7 @@ def llmint8_expert_combine(Y: torch.Tensor, positions: torch.Tensor, weights: to
         _operand(out, dtype, (T, N), "out", index)
 
     def call(st):
-        o = torch.empty((T, N), dtype=dtype, device=Y.device) if out is None else out
+        o = torch.empty(T, N, dtype=dtype, device=Y.device) if out is None else out
         rc = load_library().llmint8_expert_combine(Y.data_ptr(), _DTYPES[Y.dtype], S, N, positions.data_ptr(),
                                                    weights.data_ptr(), T, k, o.data_ptr(), code, st)
         if rc:
