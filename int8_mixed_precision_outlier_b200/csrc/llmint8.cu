@@ -75,18 +75,17 @@ cudaError_t set_attributes() {
 
 // Shared-memory limits of the products with token and channel scales and of
 // the expert positions.
-template <bool PAIR>
 cudaError_t set_product_attributes() {
   cudaError_t e = cudaSuccess;
   auto big = [&](auto kern, int bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  big(product::product_kernel<PAIR, false, product::kF16>, product::SMEM_BYTES);
-  big(product::product_kernel<PAIR, false, product::kBF16>, product::SMEM_BYTES);
-  big(product::product_kernel<PAIR, false, product::kF32>, product::SMEM_BYTES);
-  big(product::product_kernel<PAIR, true, product::kF16>, product::SMEM_BYTES);
-  big(product::product_kernel<PAIR, true, product::kBF16>, product::SMEM_BYTES);
-  big(product::product_kernel<PAIR, true, product::kF32>, product::SMEM_BYTES);
+  big(product::product_kernel<false, product::kF16>, product::SMEM_BYTES);
+  big(product::product_kernel<false, product::kBF16>, product::SMEM_BYTES);
+  big(product::product_kernel<false, product::kF32>, product::SMEM_BYTES);
+  big(product::product_kernel<true, product::kF16>, product::SMEM_BYTES);
+  big(product::product_kernel<true, product::kBF16>, product::SMEM_BYTES);
+  big(product::product_kernel<true, product::kF32>, product::SMEM_BYTES);
   big(expert::expert_positions_kernel<int32_t>, expert::pos_smem_bytes(product::MAX_GROUPS));
   big(expert::expert_positions_kernel<int64_t>, expert::pos_smem_bytes(product::MAX_GROUPS));
   return e;
@@ -110,7 +109,7 @@ int device_info(int* num_sms, int* max_pairs = nullptr) {
       return;
     }
     if (set_attributes<false>() != cudaSuccess || set_attributes<true>() != cudaSuccess ||
-        set_product_attributes<false>() != cudaSuccess || set_product_attributes<true>() != cudaSuccess) {
+        set_product_attributes() != cudaSuccess) {
       d.status = LLMINT8_ERR_CUDA;
       return;
     }
@@ -637,57 +636,74 @@ bool float_dtype(int d) { return d == LLMINT8_F16 || d == LLMINT8_BF16 || d == L
 // ragged groups it plans for equally long ones, and the kernel takes whatever
 // lengths the device's offsets give.
 struct ProductPlan {
-  bool pair = false;
   int BT = 0, quarter = 0, b_rows = 0, KPB = 0, H = 0, stages = 0, nN = 0;
   int64_t tiles = 0;  // an upper bound
 };
 
-ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, int num_sms, int max_pairs) {
-  ProductPlan best;
+ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, int max_pairs) {
   const int groups = grouped ? std::min(E, S) : 1;
-  const int avg = (S + groups - 1) / groups;
+  const int avg = (S + groups - 1) / groups;  // tokens of a group
   const bool ksplit = K % product::BK == 0;
   const int KB = (K + product::BK - 1) / product::BK;
-  best.pair = avg > 128;
-  const int want = (grouped ? 2 * avg : avg);
-  int BT = want >= product::MAX_BT ? product::MAX_BT : (want + 15) / 16 * 16;
-  best.BT = BT;
-  if (best.pair) {
-    best.H = product::BM;
-    best.nN = (N + 2 * best.H - 1) / (2 * best.H);
-  } else {
-    const int step = gated ? 32 : 8;
-    double best_cost = -1.0;
-    for (int H = step; H <= product::BM; H += step) {
-      const int nN = (N + H - 1) / H;
-      const int64_t tiles = static_cast<int64_t>(groups) * ((avg + BT - 1) / BT) * nN;
-      const double cost = static_cast<double>((tiles + num_sms - 1) / num_sms) * (H + BT + 32);
-      if (best_cost < 0.0 || cost <= best_cost) {
-        best_cost = cost;
-        best.H = H;
-        best.nN = nN;
-      }
+  auto up16 = [](int x) { return (x + 15) / 16 * 16; };
+  ProductPlan best;
+  // A CTA pair runs its tiles one after the other, `rounds` in all; a tile
+  // costs KB steps.  A step was measured at 0.04 us + 1.04 ns a token column
+  // (the MMA's own time: its rate does not fall with fewer weight rows) + 0.4
+  // ns a weight row of the CTA (the copies; below 64 rows they cost no less):
+  // 333 x 13824 x 5120 takes 24.4 us with 2 rounds of 176 x 192, 29.3 with 176
+  // x 256, 27.5 with 3 rounds of 96 x 256.
+  double best_cost = -1.0;
+  auto consider = [&](int H, int nN, int BT, int mt) {
+    const double tiles = static_cast<double>(groups) * mt * nN / max_pairs;
+    // many tiles of different lengths even out
+    const double rounds = grouped && tiles > 4.0 ? tiles : std::ceil(tiles);
+    const int cols = up16((avg + mt - 1) / mt);
+    const double cost = rounds * (KB * (0.04 + 0.00104 * cols + 0.0004 * std::max(H, 64)) + 0.5);
+    if (best_cost < 0.0 || cost <= best_cost) {
+      best_cost = cost;
+      best.H = H;
+      best.BT = BT;
+      best.nN = nN;
+    }
+  };
+  const int step = gated ? 32 : 8;
+  for (int H = step; H <= product::BM; H += step) {
+    const int nN = (N + 2 * H - 1) / (2 * H);
+    if (grouped) {
+      // room for groups twice as long as the average without a second tile
+      const int BT = std::min(product::MAX_BT, up16(std::min(2 * avg, product::MAX_BT) + 16));
+      consider(H, nN, BT, (avg + BT - 1) / BT);
+    } else {
+      const int least = (avg + product::MAX_BT - 1) / product::MAX_BT;
+      for (int mt = least; mt <= least + 8 && (mt == least || avg > 32 * (mt - 1)); ++mt)
+        consider(H, nN, up16((avg + mt - 1) / mt), mt);
     }
   }
-  const int mine = best.pair ? BT / 2 : BT;
+  best.tiles = (static_cast<int64_t>(S) / best.BT + groups) * best.nN;
+  const int mine = best.BT / 2;  // token rows of a CTA
   best.quarter = (mine + 31) / 32 * 8;
   best.b_rows = (mine + best.quarter - 1) / best.quarter * best.quarter;
-  best.tiles = (static_cast<int64_t>(S) / BT + groups) * best.nN;
+  // k-blocks per stage: a stage costs the issuing warps about 300 cycles and
+  // its products 2 a token column and k-block (160 at least), so stages of
+  // narrow tiles hold more; four stages at least, or the loads wait.
+  // 16 x 4096 x 4096: 11.1, 8.2, 7.3 us with 1, 2, 4 k-blocks.
+  const int cols = std::min(best.BT, up16(avg));
+  const int wish = cols >= 224 ? 1 : cols >= 96 ? 2 : product::KPB_MAX;
   const int kblock = (best.H + best.b_rows) * product::BK;
-  // at least three stages of as many k-blocks as possible
   best.KPB = 1;
-  while (ksplit && best.KPB < product::KPB_MAX && 2 * best.KPB <= KB && 3 * 2 * best.KPB * kblock <= product::RING_BYTES)
+  while (ksplit && best.KPB < wish && 2 * best.KPB <= KB && 4 * 2 * best.KPB * kblock <= product::RING_BYTES)
     best.KPB *= 2;
   best.stages = std::min(product::MAX_STAGES, product::RING_BYTES / (kblock * best.KPB));
   return best;
 }
 
 using ProductKernel = void (*)(const CUtensorMap, const product::TokenMaps, const product::Params);
-template <bool PAIR, bool GATED>
+template <bool GATED>
 ProductKernel product_kernel_for(int dtype) {
-  return dtype == LLMINT8_F16    ? product::product_kernel<PAIR, GATED, product::kF16>
-         : dtype == LLMINT8_BF16 ? product::product_kernel<PAIR, GATED, product::kBF16>
-                                 : product::product_kernel<PAIR, GATED, product::kF32>;
+  return dtype == LLMINT8_F16    ? product::product_kernel<GATED, product::kF16>
+         : dtype == LLMINT8_BF16 ? product::product_kernel<GATED, product::kBF16>
+                                 : product::product_kernel<GATED, product::kF32>;
 }
 
 int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const int32_t* offsets, bool grouped,
@@ -702,11 +718,11 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || misaligned4(sx) || misaligned4(sw) ||
       misaligned4(bias) || misaligned4(offsets))
     return LLMINT8_ERR_ALIGNMENT;
-  int num_sms = 0, max_pairs = 0;
-  const int rc = device_info(&num_sms, &max_pairs);
+  int max_pairs = 0;
+  const int rc = device_info(nullptr, &max_pairs);
   if (rc != LLMINT8_OK) return rc;
   const ProductPlan plan = plan_product(static_cast<int>(S), static_cast<int>(N), static_cast<int>(K),
-                                        static_cast<int>(E), grouped, gated != 0, num_sms, max_pairs);
+                                        static_cast<int>(E), grouped, gated != 0, max_pairs);
   if (plan.tiles > INT32_MAX - 4096) return LLMINT8_ERR_INVALID_ARG;
   product::Params p;
   p.S = static_cast<int>(S);
@@ -752,12 +768,10 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   for (int i = 0; i < 4; ++i)
     if (i < least || i * p.quarter >= p.b_rows) tx.m[i] = tx.m[least];
   if (!ok) return LLMINT8_ERR_CUDA;
-  const ProductKernel kern = plan.pair ? (gated ? product_kernel_for<true, true>(dtype) : product_kernel_for<true, false>(dtype))
-                                       : (gated ? product_kernel_for<false, true>(dtype) : product_kernel_for<false, false>(dtype));
-  const int units = static_cast<int>(std::min<int64_t>(plan.pair ? max_pairs : num_sms, plan.tiles));
-  const cudaError_t e = launch_ex(kern, dim3(plan.pair ? 2 * units : units), dim3(product::THREADS),
-                                  product::SMEM_BYTES, static_cast<cudaStream_t>(stream), true, plan.pair ? 2 : 1, tw,
-                                  tx, p);
+  const ProductKernel kern = gated ? product_kernel_for<true>(dtype) : product_kernel_for<false>(dtype);
+  const int pairs = static_cast<int>(std::min<int64_t>(max_pairs, plan.tiles));
+  const cudaError_t e = launch_ex(kern, dim3(2 * pairs), dim3(product::THREADS), product::SMEM_BYTES,
+                                  static_cast<cudaStream_t>(stream), true, 2, tw, tx, p);
   return e == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA;
 }
 

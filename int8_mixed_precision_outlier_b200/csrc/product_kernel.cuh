@@ -374,12 +374,14 @@ __device__ __forceinline__ int quarters_of(const Params& p, int rows) {
 // the same channels, so that lanes l and l + 16 of a warp hold the two halves
 // of one output.  OT: output type.
 //
-// PAIR: a 2-CTA cluster works on one tile of 2 H weight rows (tcgen05
-// cta_group::2, M = 256): CTA r holds weight rows H r .. of the tile and half
-// of its tokens as operands, and after the products H rows by all tokens in
-// its TMEM.  The even CTA's thread issues the MMAs; both CTAs' copies complete
-// on its `full` barriers, and each commit arrives at both CTAs.
-template <bool PAIR, bool GATED, int OT>
+// A 2-CTA cluster works on one tile of 2 H weight rows (tcgen05 cta_group::2,
+// M = 256): CTA r holds weight rows H r .. of the tile and half of its tokens
+// as operands, and after the products H rows by all tokens in its TMEM.  The
+// even CTA's elected thread issues the MMAs; both CTAs' copies complete on its
+// `full` barriers, and each commit arrives at both CTAs.  (Single CTAs with
+// tiles of 128 rows were within 3 % of pairs on the smallest shapes, up to
+// 27 % behind on others.)
+template <bool GATED, int OT>
 __global__ void __launch_bounds__(THREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ TokenMaps tmaps_x,
                    const Params p) {
@@ -401,9 +403,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
-  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-  const int units = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int unit = static_cast<int>(blockIdx.x >> 1);
+  const int units = static_cast<int>(gridDim.x >> 1);
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmap_w);
@@ -414,25 +416,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], (PAIR ? 2 : 1) * EPI_WARPS);
+      mbar_init(&tempty[b], 2 * EPI_WARPS);
     }
     mbar_init(done, 1);
     fence_barrier_init();
   }
   __syncwarp();
   if (warp == 1) {
-    if constexpr (PAIR) {
-      tmem_alloc_pair(tmem_slot, TMEM_COLS);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, TMEM_COLS);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(tmem_slot, TMEM_COLS);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncwarp();
-  if constexpr (PAIR)
-    cluster_sync();  // both CTAs' barriers are initialised before a copy or commit reaches them
+  cluster_sync();  // both CTAs' barriers are initialised before a copy or commit reaches them
   // The codes, scales and offsets may come from the kernel before this one,
   // and so may the weights (a user may have quantised them just now): nothing
   // is read before that kernel is done.  Only then may the next one start, so
@@ -460,33 +456,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (Walk t(p, groups, unit, units); ok && t.more(); t.next(p, groups)) {
       const int cols = (t.tokens() + 15) / 16 * 16;  // MMA N
-      const int mine = PAIR ? cols / 2 : cols;       // token rows this CTA copies
+      const int mine = cols / 2;                     // token rows this CTA copies
       const int x0 = t.row() + rank * mine;
       const int quarters = quarters_of(p, mine);
       const CUtensorMap* tmap_x = &tmaps_x.m[quarters - 1];
-      const int wt = PAIR ? 2 * t.nt + rank : t.nt;  // this CTA's weight rows, in units of H
-      const uint32_t tx = static_cast<uint32_t>((PAIR ? 2 : 1) * p.KPB * (a_bytes + quarters * p.quarter * BK));
+      const int wt = 2 * t.nt + rank;  // this CTA's weight rows, in units of H
+      const uint32_t tx = static_cast<uint32_t>(2 * p.KPB * (a_bytes + quarters * p.quarter * BK));
       for (int u = 0; u < p.NU; ++u, ++it) {
         ok = mbar_wait_stage(&empty[s], phase, p.wait_ns, kErrTimeoutProducer);
         if (!ok) break;
         if (issuer) {
           const int kb = p.ksplit ? u * p.KPB : 0, x = p.ksplit ? 0 : u * BK;
-          if constexpr (PAIR) {
-            const uint32_t bar = map_shared_rank(&full[s], 0);
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
-            if constexpr (GATED)
-              tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.g, wt * (p.H / 32), kb);
-            else
-              tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.g);
-            tma_load_3d_pair(stage_b(s), tmap_x, bar, x, x0, kb);
-          } else {
-            mbar_arrive_expect_tx(&full[s], tx);
-            if constexpr (GATED)
-              tma_load_5d(stage_a(s), &tmap_w, &full[s], x, 0, 2 * t.g, wt * (p.H / 32), kb);
-            else
-              tma_load_4d(stage_a(s), &tmap_w, &full[s], x, wt * p.H, kb, t.g);
-            tma_load_3d(stage_b(s), tmap_x, &full[s], x, x0, kb);
-          }
+          const uint32_t bar = map_shared_rank(&full[s], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
+          if constexpr (GATED)
+            tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.g, wt * (p.H / 32), kb);
+          else
+            tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.g);
+          tma_load_3d_pair(stage_b(s), tmap_x, bar, x, x0, kb);
         }
         if (++s == p.stages) {
           s = 0;
@@ -494,17 +481,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-    // Leave no copy in flight: wait for the last loads of every stage (in a
-    // pair the `done` commit covers the copies of both CTAs).
-    if constexpr (!PAIR) {
-      for (int i = min(it, p.stages); i > 0; --i) {
-        if (--s < 0) {
-          s = p.stages - 1;
-          phase ^= 1;
-        }
-        mbar_wait_stage(&full[s], phase ^ 1, p.wait_ns, kErrTimeoutProducer);
-      }
-    }
+    // Every copy of both CTAs has landed once the MMAs that read it are done:
+    // the `done` commit covers that.
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const bool issuer = elect_one();
@@ -515,12 +493,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = true;
       for (Walk t(p, groups, unit, units); ok && t.more(); t.next(p, groups), ++tc) {
         const int cols = (t.tokens() + 15) / 16 * 16;
-        const uint32_t idesc = idesc_i8_s32(PAIR ? 2 * BM : BM, cols);
+        const uint32_t idesc = idesc_i8_s32(2 * BM, cols);
         // k-blocks of a stage lie as the copy put them: its rows apart
-        const uint32_t b_step = static_cast<uint32_t>(quarters_of(p, PAIR ? cols / 2 : cols) * p.quarter * BK) >> 4;
+        const uint32_t b_step = static_cast<uint32_t>(quarters_of(p, cols / 2) * p.quarter * BK) >> 4;
         const int buf = tc & 1;
         if (tc >= 2) {
-          ok = mbar_wait_stage<PAIR>(&tempty[buf], ((tc >> 1) - 1) & 1, p.wait_ns, kErrTimeoutMma);
+          ok = mbar_wait_stage<true>(&tempty[buf], ((tc >> 1) - 1) & 1, p.wait_ns, kErrTimeoutMma);
           if (!ok) break;
         }
         tc_fence_after();
@@ -534,14 +512,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t blow = sdesc_low(ring + s * stage_bytes);
             uint32_t alow = sdesc_low(ring + s * stage_bytes + p.KPB * b_bytes);
             for (int j = 0; j < nkb; ++j, alow += a_bytes >> 4, blow += b_step) {
-              mma_i8_low<PAIR>(d, alow, blow, idesc, (u > 0 || j > 0) ? 1u : 0u);
+              mma_i8_low_pair(d, alow, blow, idesc, (u > 0 || j > 0) ? 1u : 0u);
 #pragma unroll
-              for (int k = 1; k < BK / 32; ++k) mma_i8_low<PAIR>(d, alow + 2 * k, blow + 2 * k, idesc, 1u);
+              for (int k = 1; k < BK / 32; ++k) mma_i8_low_pair(d, alow + 2 * k, blow + 2 * k, idesc, 1u);
             }
-            if constexpr (PAIR)
-              mma_commit_pair(&empty[s], 0x3);
-            else
-              mma_commit(&empty[s]);
+            mma_commit_pair(&empty[s], 0x3);
           }
           if (++s == p.stages) {
             s = 0;
@@ -549,17 +524,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         if (ok && issuer) {
-          if constexpr (PAIR)
-            mma_commit_pair(&tfull[buf], 0x3);
-          else
-            mma_commit(&tfull[buf]);
+          mma_commit_pair(&tfull[buf], 0x3);
         }
       }
       if (issuer) {
-        if constexpr (PAIR)
-          mma_commit_pair(done, 0x3);
-        else
-          mma_commit(done);
+        mma_commit_pair(done, 0x3);
       }
     }
     // The MMAs (of both CTAs) are complete before TMEM is released.
@@ -584,7 +553,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       Ahead a;
       a.m0 = t.row();
       a.tok = t.tokens();
-      a.c = (PAIR ? 2 * t.nt + rank : t.nt) * tile_ch + q * Epi::CH;
+      a.c = (2 * t.nt + rank) * tile_ch + q * Epi::CH;
       a.n = min(min(tile_ch - q * Epi::CH, Epi::CH), p.No - a.c);
       a.sx = etid < a.tok ? p.sx[a.m0 + etid] : 0.0f;
 #pragma unroll
@@ -627,32 +596,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       // write them.
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR)
-          mbar_arrive_remote(map_shared_rank(&tempty[buf], 0));
-        else
-          mbar_arrive(&tempty[buf]);
-      }
+      if (lane == 0) mbar_arrive_remote(map_shared_rank(&tempty[buf], 0));
     }
   }
 
   __syncwarp();
   tc_fence_before();
-  if constexpr (PAIR) {
-    // Neither CTA leaves while the other may still signal its barriers or,
-    // after a timeout, copies of the pair may still be landing.
-    if (threadIdx.x == 0 && ld_error_word() != 0) sleep_ns_bounded(20000);
-    __syncwarp();
-    cluster_sync();
-  } else {
-    __syncthreads();
-  }
+  // Neither CTA leaves while the other may still signal its barriers or, after
+  // a timeout, copies of the pair may still be landing.
+  if (threadIdx.x == 0 && ld_error_word() != 0) sleep_ns_bounded(20000);
+  __syncwarp();
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (PAIR)
-      tmem_dealloc_pair(tmem_base, TMEM_COLS);
-    else
-      tmem_dealloc(tmem_base, TMEM_COLS);
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
 }
 
