@@ -86,8 +86,16 @@ cudaError_t set_product_attributes() {
   big(product::product_kernel<true, product::kF16>, product::SMEM_BYTES);
   big(product::product_kernel<true, product::kBF16>, product::SMEM_BYTES);
   big(product::product_kernel<true, product::kF32>, product::SMEM_BYTES);
-  big(expert::expert_positions_kernel<int32_t>, expert::pos_smem_bytes(product::MAX_GROUPS));
-  big(expert::expert_positions_kernel<int64_t>, expert::pos_smem_bytes(product::MAX_GROUPS));
+  auto positions = [&](auto kern) {
+    big(kern, expert::pos_smem_bytes(product::MAX_GROUPS));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  };
+  positions(expert::expert_positions_kernel<int32_t, 1>);
+  positions(expert::expert_positions_kernel<int32_t, 4>);
+  positions(expert::expert_positions_kernel<int32_t, 0>);
+  positions(expert::expert_positions_kernel<int64_t, 1>);
+  positions(expert::expert_positions_kernel<int64_t, 4>);
+  positions(expert::expert_positions_kernel<int64_t, 0>);
   return e;
 }
 
@@ -778,12 +786,13 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
 template <int IT>
 cudaError_t launch_quantize_rows(const void* X, int T, int K, const int32_t* positions, int copies, int S,
                                  int8_t* Xq, float* xscale, cudaStream_t st) {
-  const int nchunk = K / 16;
-  const int threads = std::min(expert::kRowThreads, (nchunk + 31) / 32 * 32);
-  const int per = (nchunk + threads - 1) / threads;
-  auto kern = per <= 1   ? expert::quantize_rows_kernel<IT, 1>
-              : per <= 2 ? expert::quantize_rows_kernel<IT, 2>
-                         : expert::quantize_rows_kernel<IT, 0>;
+  // A chunk a thread for rows of up to 256, then two, then as many as it takes.
+  const int nchunk = K / expert::kChunk<IT>;
+  const int want = nchunk <= 256 ? nchunk : (nchunk + 1) / 2;
+  const int threads = std::min(expert::kRowThreads, (want + 31) / 32 * 32);
+  auto kern = nchunk <= threads       ? expert::quantize_rows_kernel<IT, 1>
+              : nchunk <= 2 * threads ? expert::quantize_rows_kernel<IT, 2>
+                                      : expert::quantize_rows_kernel<IT, 0>;
   return launch(kern, dim3(static_cast<unsigned>(T)), dim3(threads), 0, st, true, X, K, positions, copies, S, Xq,
                 xscale);
 }
@@ -808,6 +817,20 @@ int quantize_rows_impl(const void* X, int dtype, int64_t T, int64_t K, const int
   return e == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA;
 }
 
+template <typename ID>
+cudaError_t launch_expert_positions(const void* ids, int64_t S, int E, int32_t* positions, int32_t* offsets,
+                                    cudaStream_t st) {
+  int ctas = 1;
+  while (ctas < expert::kPosMaxCtas && S > static_cast<int64_t>(ctas) * expert::kPosThreads) ctas *= 2;
+  const int64_t warps = static_cast<int64_t>(ctas) * expert::kPosWarps;
+  const int64_t per_warp = ((S + warps - 1) / warps + 31) / 32 * 32;
+  auto kern = per_warp <= 32    ? expert::expert_positions_kernel<ID, 1>
+              : per_warp <= 128 ? expert::expert_positions_kernel<ID, 4>
+                                : expert::expert_positions_kernel<ID, 0>;
+  return launch_ex(kern, dim3(ctas), dim3(expert::kPosThreads), static_cast<size_t>(expert::pos_smem_bytes(E)), st,
+                   true, ctas, static_cast<const ID*>(ids), S, E, per_warp, positions, offsets);
+}
+
 int expert_positions_impl(const void* ids, int id_bytes, int64_t T, int64_t k, int64_t E, int32_t* positions,
                           int32_t* offsets, void* stream) {
   if (T < 0 || k < 1 || T > INT32_MAX || k > INT32_MAX || T * k > INT32_MAX - 64) return LLMINT8_ERR_INVALID_ARG;
@@ -819,19 +842,10 @@ int expert_positions_impl(const void* ids, int id_bytes, int64_t T, int64_t k, i
     return LLMINT8_ERR_ALIGNMENT;
   const int rc = device_info(nullptr);
   if (rc != LLMINT8_OK) return rc;
-  int ctas = 1;
-  while (ctas < expert::kPosMaxCtas && S > static_cast<int64_t>(ctas) * 4 * expert::kPosThreads) ctas *= 2;
-  const int64_t warps = static_cast<int64_t>(ctas) * expert::kPosWarps;
-  const int64_t per_warp = ((S + warps - 1) / warps + 31) / 32 * 32;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t smem = static_cast<size_t>(expert::pos_smem_bytes(static_cast<int>(E)));
-  const int e_ = static_cast<int>(E);
   const cudaError_t e =
-      id_bytes == 4
-          ? launch_ex(expert::expert_positions_kernel<int32_t>, dim3(ctas), dim3(expert::kPosThreads), smem, st, true,
-                      ctas, static_cast<const int32_t*>(ids), S, e_, per_warp, positions, offsets)
-          : launch_ex(expert::expert_positions_kernel<int64_t>, dim3(ctas), dim3(expert::kPosThreads), smem, st, true,
-                      ctas, static_cast<const int64_t*>(ids), S, e_, per_warp, positions, offsets);
+      id_bytes == 4 ? launch_expert_positions<int32_t>(ids, S, static_cast<int>(E), positions, offsets, st)
+                    : launch_expert_positions<int64_t>(ids, S, static_cast<int>(E), positions, offsets, st);
   return e == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA;
 }
 
@@ -852,7 +866,7 @@ int expert_combine_impl(const void* Y, int y_dtype, int64_t S, int64_t N, const 
   if (!aligned16(Y) || !aligned16(out) || misaligned4(positions) || misaligned4(weights))
     return LLMINT8_ERR_ALIGNMENT;
   const bool vec = N % 8 == 0;
-  const int64_t cols = (N + (vec ? 8 : 1) * expert::kCombineThreads - 1) / ((vec ? 8 : 1) * expert::kCombineThreads);
+  const int64_t cols = (N + 8 * expert::kCombineThreads - 1) / (8 * expert::kCombineThreads);
   if (cols > 65535) return LLMINT8_ERR_INVALID_ARG;
   const int rc = device_info(nullptr);
   if (rc != LLMINT8_OK) return rc;
