@@ -688,6 +688,8 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
         consider(H, nN, up16((avg + mt - 1) / mt), mt);
     }
   }
+  if (const char* v = getenv("PP_BT")) best.BT = atoi(v);  // TUNE
+  if (const char* v = getenv("PP_H")) best.H = atoi(v), best.nN = (N + 2 * best.H - 1) / (2 * best.H);  // TUNE
   best.tiles = (static_cast<int64_t>(S) / best.BT + groups) * best.nN;
   const int mine = best.BT / 2;  // token rows of a CTA
   best.quarter = (mine + 31) / 32 * 8;
@@ -702,6 +704,7 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   best.KPB = 1;
   while (ksplit && best.KPB < wish && 2 * best.KPB <= KB && 4 * 2 * best.KPB * kblock <= product::RING_BYTES)
     best.KPB *= 2;
+  if (getenv("PP_KPB")) best.KPB = atoi(getenv("PP_KPB"));  // TUNE
   best.stages = std::min(product::MAX_STAGES, product::RING_BYTES / (kblock * best.KPB));
   return best;
 }

@@ -15,7 +15,8 @@ import torch
 
 from .llmint8 import _check, _need, load_library
 
-_F16, _BF16, _F32, _I8, _I32 = torch.float16, torch.bfloat16, torch.float32, torch.int8, torch.int32
+_F16, _BF16, _F32 = torch.float16, torch.bfloat16, torch.float32
+_I8, _I32, _I64 = torch.int8, torch.int32, torch.int64
 _DTYPES = {_F16: 0, _BF16: 1, _F32: 2}
 MAX_EXPERTS = 1024
 
@@ -81,17 +82,41 @@ def llmint8_quantize_rows(X: torch.Tensor, positions: torch.Tensor | None = None
     Xq is given, and rows that no position names are left as they were.
     Positions must be distinct.  A row with a NaN or an infinity gets the scale
     NaN and codes 0."""
+    try:
+        T, K = X.shape
+        S = T
+        if positions is not None:
+            copies = positions.shape[1]
+            S = T * copies if Xq is None else Xq.shape[0]
+        index = X.get_device()
+        # _check_quantize in one expression
+        fine = (index >= 0 and X.dtype in _DTYPES and X.is_contiguous()
+                and (positions is None or copies > 0 and positions.dtype is _I32 and positions.shape == (T, copies)
+                     and positions.is_contiguous() and positions.get_device() == index)
+                and (Xq is None or Xq.dtype is _I8 and Xq.shape == (S, K) and Xq.is_contiguous()
+                     and Xq.get_device() == index)
+                and (xscale is None or xscale.dtype is _F32 and xscale.shape == (S,) and xscale.is_contiguous()
+                     and xscale.get_device() == index))
+    except (AttributeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _check_quantize(X, positions, Xq, xscale)
+    if stream is not None or index != _current_device():
+        return _run(index, stream, lambda st: _launch_quantize(X, positions, Xq, xscale, S, st))
+    return _launch_quantize(X, positions, Xq, xscale, S, _raw_stream(index))
+
+
+def _check_quantize(X, positions, Xq, xscale):
+    """Raises for what is wrong with llmint8_quantize_rows' arguments, one by one."""
     index = _first(X, None, 2, "X")
     T, K = X.shape
-    copies, S, at = 0, T, None
+    S = T
     if positions is not None:
         _first(positions, (_I32,), 2, "positions")
-        copies = positions.shape[1]
-        _operand(positions, _I32, (T, copies), "positions", index)
-        if copies < 1:
+        _operand(positions, _I32, (T, positions.shape[1]), "positions", index)
+        if positions.shape[1] < 1:
             raise ValueError("positions must have a column")
-        at = positions.data_ptr()
-        S = T * copies
+        S = positions.numel()
         if Xq is not None:
             _first(Xq, (_I8,), 2, "Xq")
             S = Xq.shape[0]
@@ -100,16 +125,19 @@ def llmint8_quantize_rows(X: torch.Tensor, positions: torch.Tensor | None = None
     if xscale is not None:
         _operand(xscale, _F32, (S,), "xscale", index)
 
-    def call(st):
-        q = torch.empty(S, K, dtype=_I8, device=X.device) if Xq is None else Xq
-        s = torch.empty(S, dtype=_F32, device=X.device) if xscale is None else xscale
-        rc = load_library().llmint8_quantize_rows(X.data_ptr(), _DTYPES[X.dtype], T, K, at, copies, S, q.data_ptr(),
-                                                  s.data_ptr(), st)
-        if rc:
-            _check(rc, "llmint8_quantize_rows")
-        return q, s
 
-    return _run(index, stream, call)
+def _launch_quantize(X, positions, Xq, xscale, S, st):
+    T, K = X.shape
+    if Xq is None:
+        Xq = torch.empty(S, K, dtype=_I8, device=X.device)
+    if xscale is None:
+        xscale = torch.empty(S, dtype=_F32, device=X.device)
+    at, copies = (None, 0) if positions is None else (positions.data_ptr(), positions.shape[1])
+    rc = load_library().llmint8_quantize_rows(X.data_ptr(), _DTYPES[X.dtype], T, K, at, copies, S, Xq.data_ptr(),
+                                              xscale.data_ptr(), st)
+    if rc:
+        _check(rc, "llmint8_quantize_rows")
+    return Xq, xscale
 
 
 def _check_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y):
@@ -211,26 +239,47 @@ def llmint8_expert_positions(ids: torch.Tensor, experts: int, positions: torch.T
     (positions int32 [T, k], offsets int32 [experts + 1]): expert e's rows are
     offsets[e] .. offsets[e + 1] - 1, stable in the order of ids; a choice
     outside [0, experts) has position -1."""
-    index = _first(ids, (_I32, torch.int64), 2, "ids")
-    T, k = ids.shape
-    experts = int(experts)
+    try:
+        T, k = ids.shape
+        index = ids.get_device()
+        # _check_positions in one expression
+        fine = (index >= 0 and (ids.dtype is _I64 or ids.dtype is _I32) and ids.is_contiguous()
+                and 0 < experts <= MAX_EXPERTS
+                and (positions is None or positions.dtype is _I32 and positions.shape == (T, k)
+                     and positions.is_contiguous() and positions.get_device() == index)
+                and (offsets is None or offsets.dtype is _I32 and offsets.shape == (experts + 1,)
+                     and offsets.is_contiguous() and offsets.get_device() == index))
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _check_positions(ids, experts, positions, offsets)
+    if stream is not None or index != _current_device():
+        return _run(index, stream, lambda st: _launch_positions(ids, experts, positions, offsets, st))
+    return _launch_positions(ids, experts, positions, offsets, _raw_stream(index))
+
+
+def _check_positions(ids, experts, positions, offsets):
+    """Raises for what is wrong with llmint8_expert_positions' arguments, one by one."""
+    index = _first(ids, (_I32, _I64), 2, "ids")
     if experts < 1 or experts > MAX_EXPERTS:
         raise ValueError(f"experts must be in [1, {MAX_EXPERTS}], got {experts}")
     if positions is not None:
-        _operand(positions, _I32, (T, k), "positions", index)
+        _operand(positions, _I32, tuple(ids.shape), "positions", index)
     if offsets is not None:
         _operand(offsets, _I32, (experts + 1,), "offsets", index)
 
-    def call(st):
-        p = torch.empty(T, k, dtype=_I32, device=ids.device) if positions is None else positions
-        o = torch.empty(experts + 1, dtype=_I32, device=ids.device) if offsets is None else offsets
-        rc = load_library().llmint8_expert_positions(ids.data_ptr(), ids.element_size(), T, k, experts, p.data_ptr(),
-                                                     o.data_ptr(), st)
-        if rc:
-            _check(rc, "llmint8_expert_positions")
-        return p, o
 
-    return _run(index, stream, call)
+def _launch_positions(ids, experts, positions, offsets, st):
+    T, k = ids.shape
+    if positions is None:
+        positions = torch.empty(T, k, dtype=_I32, device=ids.device)
+    if offsets is None:
+        offsets = torch.empty(experts + 1, dtype=_I32, device=ids.device)
+    rc = load_library().llmint8_expert_positions(ids.data_ptr(), 8 if ids.dtype is _I64 else 4, T, k, experts,
+                                                 positions.data_ptr(), offsets.data_ptr(), st)
+    if rc:
+        _check(rc, "llmint8_expert_positions")
+    return positions, offsets
 
 
 def llmint8_expert_combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor, dtype=None,
@@ -238,23 +287,87 @@ def llmint8_expert_combine(Y: torch.Tensor, positions: torch.Tensor, weights: to
     """out [T, N]: out[t] = sum_j weights[t, j] Y[positions[t, j]] over the
     positions >= 0 (Y [S, N], positions int32 [T, k], weights float32 [T, k]),
     in `dtype` (Y's by default, or out's)."""
+    try:
+        N = Y.shape[1]
+        shape = positions.shape
+        T, k = shape
+        dtype = out.dtype if out is not None else Y.dtype if dtype is None else dtype
+        index = Y.get_device()
+        # _check_combine in one expression
+        fine = (index >= 0 and Y.dtype in _DTYPES and dtype in _DTYPES and Y.ndim == 2 and Y.is_contiguous()
+                and positions.dtype is _I32 and positions.is_contiguous() and positions.get_device() == index
+                and weights.dtype is _F32 and weights.shape == shape and weights.is_contiguous()
+                and weights.get_device() == index
+                and (out is None or out.shape == (T, N) and out.is_contiguous() and out.get_device() == index))
+    except (AttributeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _check_combine(Y, positions, weights, dtype, out)
+    if stream is not None or index != _current_device():
+        return _run(index, stream, lambda st: _launch_combine(Y, positions, weights, dtype, out, st))
+    return _launch_combine(Y, positions, weights, dtype, out, _raw_stream(index))
+
+
+def _check_combine(Y, positions, weights, dtype, out):
+    """Raises for what is wrong with llmint8_expert_combine's arguments, one by one."""
     index = _first(Y, None, 2, "Y")
     _first(positions, (_I32,), 2, "positions")
+    shape = tuple(positions.shape)
+    _operand(positions, _I32, shape, "positions", index)
+    _operand(weights, _F32, shape, "weights", index)
+    _out_dtype(out.dtype if out is not None else Y.dtype if dtype is None else dtype)
+    if out is not None:
+        _operand(out, out.dtype, (shape[0], Y.shape[1]), "out", index)
+
+
+def _launch_combine(Y, positions, weights, dtype, out, st):
     S, N = Y.shape
     T, k = positions.shape
-    _operand(positions, _I32, (T, k), "positions", index)
-    _operand(weights, _F32, (T, k), "weights", index)
-    dtype = out.dtype if out is not None else Y.dtype if dtype is None else dtype
-    code = _out_dtype(dtype)
-    if out is not None:
-        _operand(out, dtype, (T, N), "out", index)
+    if out is None:
+        out = torch.empty(T, N, dtype=dtype, device=Y.device)
+    rc = load_library().llmint8_expert_combine(Y.data_ptr(), _DTYPES[Y.dtype], S, N, positions.data_ptr(),
+                                               weights.data_ptr(), T, k, out.data_ptr(), _DTYPES[dtype], st)
+    if rc:
+        _check(rc, "llmint8_expert_combine")
+    return out
 
-    def call(st):
-        o = torch.empty(T, N, dtype=dtype, device=Y.device) if out is None else out
-        rc = load_library().llmint8_expert_combine(Y.data_ptr(), _DTYPES[Y.dtype], S, N, positions.data_ptr(),
-                                                   weights.data_ptr(), T, k, o.data_ptr(), code, st)
-        if rc:
-            _check(rc, "llmint8_expert_combine")
-        return o
 
-    return _run(index, stream, call)
+class Int8Experts:
+    """A mixture of gated experts with int8 weights:
+
+        y[t] = sum_j weights[t, j] W2[e] (silu(G[e] x[t]) * (V[e] x[t])),  e = ids[t, j],  W1[e] = [G[e]; V[e]]
+
+    W1 [E, 2 F, K] and W2 [E, N, F] (float16, bfloat16 or float32, K and F
+    multiples of 16) are quantised once, per output channel; activations per
+    row, before each product.  A call takes X [T, K], a router's ids [T, k]
+    (int32 or int64; outside [0, E): no expert) and weights [T, k] (float32)
+    and returns [T, N] in X's type.  The hidden rows stay in float32 until they
+    are quantised: rounding them to 16 bits first would move their codes.  The
+    experts' outputs are rounded to X's type before the weighted sum, which
+    halves what the combine reads and costs one rounding per term.  Buffers are
+    allocated by each call on its stream, so calls on several streams and
+    captured graphs do not meet.
+    """
+
+    def __init__(self, W1: torch.Tensor, W2: torch.Tensor):
+        if W1.dim() != 3 or W2.dim() != 3 or W1.shape[0] != W2.shape[0] or W1.shape[1] != 2 * W2.shape[2]:
+            raise ValueError(f"W1 must be [E, 2 F, K] and W2 [E, N, F], got {tuple(W1.shape)} and {tuple(W2.shape)}")
+        self.E, two_f, self.K = W1.shape
+        self.N, self.F = W2.shape[1:]
+        if self.K % 16 or self.F % 16:
+            raise ValueError(f"K and F must be multiples of 16, got {self.K} and {self.F}")
+        q, s = llmint8_quantize_rows(W1.reshape(-1, self.K).contiguous())
+        self.W1q, self.W1scale = q.view(self.E, two_f, self.K), s.view(self.E, two_f)
+        q, s = llmint8_quantize_rows(W2.reshape(-1, self.F).contiguous())
+        self.W2q, self.W2scale = q.view(self.E, self.N, self.F), s.view(self.E, self.N)
+
+    def resident_weight_bytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.W1q, self.W1scale, self.W2q, self.W2scale))
+
+    def __call__(self, X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, stream=None) -> torch.Tensor:
+        positions, offsets = llmint8_expert_positions(ids, self.E, stream=stream)
+        Xq, xscale = llmint8_quantize_rows(X, positions, stream=stream)
+        H = llmint8_grouped_matmul(Xq, xscale, offsets, self.W1q, self.W1scale, gated=True, dtype=_F32, stream=stream)
+        Hq, hscale = llmint8_quantize_rows(H, stream=stream)
+        Y = llmint8_grouped_matmul(Hq, hscale, offsets, self.W2q, self.W2scale, dtype=X.dtype, stream=stream)
+        return llmint8_expert_combine(Y, positions, weights, stream=stream)

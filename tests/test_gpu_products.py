@@ -561,3 +561,81 @@ def test_empty_calls(L):
     assert L.llmint8_expert_combine(Y, pos, torch.empty(0, 2, device="cuda")).shape == (0, 16)
     pos = torch.full((4, 2), -1, dtype=torch.int32, device="cuda")
     assert not L.llmint8_expert_combine(Y[:0], pos, torch.ones(4, 2, device="cuda")).any()
+
+
+# ------------------------------------------------------------------ the layer
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,k,E,K,F,N", [(1, 2, 4, 128, 64, 128), (75, 3, 8, 256, 96, 200)])
+def test_int8_experts(L, dtype, T, k, E, K, F, N):
+    """The layer is the five calls, bit for bit, and near the layer in 64 bits: with codes within half a step of
+    everything that is quantised (weights, x, hidden rows), each of the three quantised factors of an output is off by
+    at most 1 / 254 of its row's maximum; the bound adds these up by absolute values."""
+    g = gen(T + K + F)
+    W1 = torch.randn(E, 2 * F, K, generator=g, device="cuda").to(dtype) / K ** 0.5
+    W2 = torch.randn(E, N, F, generator=g, device="cuda").to(dtype) / F ** 0.5
+    X = torch.randn(T, K, generator=g, device="cuda").to(dtype)
+    ids = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices
+    w = torch.softmax(torch.randn(T, k, generator=g, device="cuda"), 1)
+    if T > 1:
+        ids[3] = E
+    layer = L.Int8Experts(W1, W2)
+    assert layer.resident_weight_bytes() == E * (2 * F * K + N * F + 4 * (2 * F + N))
+    out = layer(X, ids, w)
+    positions, offsets = L.llmint8_expert_positions(ids, E)
+    Xq, sx = L.llmint8_quantize_rows(X, positions)
+    H = L.llmint8_grouped_matmul(Xq, sx, offsets, layer.W1q, layer.W1scale, gated=True, dtype=torch.float32)
+    Hq, sh = L.llmint8_quantize_rows(H)
+    Y = L.llmint8_grouped_matmul(Hq, sh, offsets, layer.W2q, layer.W2scale, dtype=dtype)
+    assert out.dtype == dtype and torch.equal(out, L.llmint8_expert_combine(Y, positions, w))
+
+    x, step = X.double(), lambda a: a.abs().amax(-1, keepdim=True) / 254 * (1 + 1e-6)  # half a code
+    want, tol = torch.zeros(T, N, device="cuda", dtype=torch.float64), torch.zeros(T, N, device="cuda", dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            if e >= E:
+                continue
+            w1, w2 = W1[e].double(), W2[e].double()
+            z = w1 @ x[t]
+            dz = step(w1)[:, 0] * (x[t].abs() + step(x[t])).sum() + w1.abs().sum(1) * step(x[t])
+            gz, u, dg, du = z[:F], z[F:], dz[:F], dz[F:]
+            h = gz * torch.sigmoid(gz) * u
+            dh = 1.1 * dg * (u.abs() + du) + (gz * torch.sigmoid(gz)).abs() * du
+            dh = dh + (h.abs() + dh).max() / 254 * (1 + 1e-6)
+            y = w2 @ h
+            dy = w2.abs() @ dh + step(w2)[:, 0] * (h.abs() + dh).sum()
+            want[t] += w[t, j].double() * y
+            tol[t] += w[t, j].double() * (dy + (y.abs() + dy) * torch.finfo(dtype).eps)
+    check(out, want, tol * (1 + 1e-3) + torch.finfo(dtype).eps * (want.abs() + tol) + HALF_SUBNORMAL[dtype])
+
+
+def test_int8_experts_refusals(L):
+    W = torch.zeros(2, 64, 32, device="cuda")
+    for W1, W2 in [(W, torch.zeros(2, 32, 64, device="cuda")), (W, torch.zeros(3, 32, 32, device="cuda")), (W[0], W),
+                   (torch.zeros(2, 48, 32, device="cuda"), torch.zeros(2, 32, 24, device="cuda")),
+                   (torch.zeros(2, 64, 24, device="cuda"), torch.zeros(2, 32, 32, device="cuda"))]:
+        with pytest.raises(ValueError):
+            L.Int8Experts(W1, W2)
+    layer = L.Int8Experts(W, torch.zeros(2, 32, 32, device="cuda"))
+    ids, w = torch.zeros(4, 1, dtype=torch.int64, device="cuda"), torch.ones(4, 1, device="cuda")
+    with pytest.raises(ValueError):
+        layer(torch.zeros(4, 48, device="cuda"), ids, w)
+    with pytest.raises(ValueError):
+        layer(torch.zeros(5, 32, device="cuda"), ids, w)
+    with pytest.raises(TypeError):
+        layer(torch.zeros(4, 32, device="cuda"), ids, w.double())
+
+
+def test_int8_experts_on_a_stream_of_its_own(L):
+    g = gen(21)
+    layer = L.Int8Experts(torch.randn(4, 256, 512, generator=g, device="cuda"), torch.randn(4, 512, 128, generator=g, device="cuda"))
+    X = torch.randn(200, 512, generator=g, device="cuda")
+    ids = torch.randint(0, 4, (200, 2), generator=g, device="cuda")
+    w = torch.rand(200, 2, generator=g, device="cuda")
+    want = layer(X, ids, w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [layer(X, ids, w, stream=s) for s in streams * 4]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
