@@ -688,8 +688,6 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
         consider(H, nN, up16((avg + mt - 1) / mt), mt);
     }
   }
-  if (const char* v = getenv("PP_BT")) best.BT = atoi(v);  // TUNE
-  if (const char* v = getenv("PP_H")) best.H = atoi(v), best.nN = (N + 2 * best.H - 1) / (2 * best.H);  // TUNE
   best.tiles = (static_cast<int64_t>(S) / best.BT + groups) * best.nN;
   const int mine = best.BT / 2;  // token rows of a CTA
   best.quarter = (mine + 31) / 32 * 8;
@@ -704,7 +702,6 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   best.KPB = 1;
   while (ksplit && best.KPB < wish && 2 * best.KPB <= KB && 4 * 2 * best.KPB * kblock <= product::RING_BYTES)
     best.KPB *= 2;
-  if (getenv("PP_KPB")) best.KPB = atoi(getenv("PP_KPB"));  // TUNE
   best.stages = std::min(product::MAX_STAGES, product::RING_BYTES / (kblock * best.KPB));
   return best;
 }
@@ -720,7 +717,8 @@ ProductKernel product_kernel_for(int dtype) {
 int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const int32_t* offsets, bool grouped,
                  int64_t E, const int8_t* Wq, const float* sw, const float* bias, int64_t N, int gated, void* Y,
                  int dtype, void* stream) {
-  if (S < 0 || N < 0 || S > INT32_MAX || N > INT32_MAX || K < 16 || K > kMaxK) return LLMINT8_ERR_INVALID_ARG;
+  if (S < 0 || N < 0 || S > INT32_MAX - product::MAX_BT || N > INT32_MAX || K < 16 || K > kMaxK)
+    return LLMINT8_ERR_INVALID_ARG;
   if (E < 1 || E > product::MAX_GROUPS || !float_dtype(dtype)) return LLMINT8_ERR_INVALID_ARG;
   if (gated && N % 32 != 0) return LLMINT8_ERR_INVALID_ARG;
   if (K % 16 != 0) return LLMINT8_ERR_ALIGNMENT;
@@ -749,8 +747,9 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   p.H = plan.H;
   p.nN = plan.nN;
   p.BT = plan.BT;
-  p.mt = grouped ? 0 : product::token_tiles(p.S, plan.BT);
-  p.per = product::tile_rows(p.S, p.mt);
+  p.count = product::tile_count(plan.BT);
+  p.mt = grouped ? 0 : product::token_tiles(p.S, p.count);
+  p.per = product::tile_rows(p.S, p.mt, plan.BT);
   p.quarter = plan.quarter;
   p.b_rows = plan.b_rows;
   p.stages = plan.stages;

@@ -56,6 +56,25 @@ static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 
 enum : int { kF16 = 0, kBF16 = 1, kF32 = 2 };
 
+// A group of m rows is cut into mt = ceil(m / BT) tiles of `per` rows (a
+// multiple of 16, at most BT; the last tile may be shorter).  BT <= 256 is the
+// same for all, so the division is a multiplication: with `shift` = 31 +
+// ceil(log2 BT) and magic = floor(2^shift / BT) + 1, the product x * magic of
+// x = m + BT - 1 < 2^31 exceeds 2^shift x / BT by at most x < 2^shift / BT, so
+// the quotient is exact; it stays below 2^64.
+struct TileCount {
+  uint64_t magic;
+  int shift, bt;
+};
+__host__ inline TileCount tile_count(int bt) {
+  int shift = 31;
+  while ((1 << (shift - 31)) < bt) ++shift;
+  return TileCount{(1ull << shift) / static_cast<uint64_t>(bt) + 1, shift, bt};
+}
+__host__ __device__ inline int token_tiles(int m, const TileCount& c) {
+  return static_cast<int>((static_cast<uint64_t>(m) + static_cast<uint64_t>(c.bt - 1)) * c.magic >> c.shift);
+}
+
 struct Params {
   int S, N, K;         // rows of Xq and Y, weight rows of a group, columns
   int No;              // columns of Y: N, or N / 2 when gated
@@ -67,6 +86,7 @@ struct Params {
   int nN;              // tiles along the channels (2 H rows each for CTA pairs)
   int BT;              // most tokens of a tile, a multiple of 16
   int mt, per;         // without offsets: token tiles, rows of each
+  TileCount count;     // of BT
   int quarter;         // token rows of a copy come in 1..4 quarters (a multiple of 8 rows each)
   int b_rows;          // token rows that a k-block of a stage has room for
   int stages;
@@ -84,10 +104,16 @@ struct TokenMaps {
   CUtensorMap m[4];
 };
 
-// A group's rows are cut into mt tiles of `per` rows (a multiple of 16; the
-// last may be shorter).
-__host__ __device__ inline int token_tiles(int m, int bt) { return (m + bt - 1) / bt; }
-__host__ __device__ inline int tile_rows(int m, int mt) { return mt ? ((m + mt - 1) / mt + 15) / 16 * 16 : 0; }
+// Equal shares up to the rounding to 16; an estimate that falls short of m is
+// raised (BT itself never does).
+__host__ __device__ inline int tile_rows(int m, int mt, int bt) {
+  if (mt <= 1) return (m + 15) / 16 * 16;
+  const int share = static_cast<int>(static_cast<float>(m) / static_cast<float>(mt)) + 1;
+  int per = (share + 15) / 16 * 16;
+  if (per > bt) per = bt;
+  if (static_cast<int64_t>(per) * mt < m) per += 16;
+  return per;
+}
 
 // The groups, in shared memory.
 struct Groups {
@@ -180,19 +206,18 @@ __device__ __forceinline__ void scan_groups(const Params& p, const Groups& s) {
     }
     return;
   }
-  int base = 0, prev = 0;  // tiles and upper bound of the groups before this chunk
-  bool bad = false;
+  // The first chunk's bounds are in flight together with the first bound.
+  const int first = p.offsets[0];
+  int o = lane < p.E ? p.offsets[lane + 1] : 0;
+  int base = 0, prev = min(max(first, 0), p.S);  // tiles and upper bound of the groups before this chunk
+  bool bad = prev != first;
   if (lane == 0) {
-    const int o = p.offsets[0];
-    prev = min(max(o, 0), p.S);
-    bad = prev != o;
     s.off[0] = prev;
     s.cum[0] = 0;
   }
-  prev = __shfl_sync(0xffffffffu, prev, 0);
   for (int g0 = 0; g0 < p.E; g0 += 32) {
     const int g = g0 + lane;
-    const int o = g < p.E ? p.offsets[g + 1] : 0;
+    const int ahead = g + 32 < p.E ? p.offsets[g + 33] : 0;
     int end = g < p.E ? min(max(o, 0), p.S) : 0;
     // a running maximum: no bound lies before an earlier one
 #pragma unroll
@@ -204,7 +229,7 @@ __device__ __forceinline__ void scan_groups(const Params& p, const Groups& s) {
     bad |= g < p.E && end != o;
     int begin = __shfl_up_sync(0xffffffffu, end, 1);
     if (lane == 0) begin = prev;
-    const int mt = token_tiles(end - begin, p.BT);
+    const int mt = token_tiles(end - begin, p.count);
     int n = g < p.E ? mt * p.nN : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -215,16 +240,42 @@ __device__ __forceinline__ void scan_groups(const Params& p, const Groups& s) {
       s.off[g + 1] = end;
       s.cum[g + 1] = base + n;
       s.mt[g] = mt;
-      s.per[g] = static_cast<uint16_t>(tile_rows(end - begin, mt));
+      s.per[g] = static_cast<uint16_t>(tile_rows(end - begin, mt, p.BT));
     }
     base += __shfl_sync(0xffffffffu, n, 31);
     prev = __shfl_sync(0xffffffffu, end, 31);
+    o = ahead;
   }
   if (bad && blockIdx.x == 0) atomicOr(&g_error_word, kErrBadIndex);
 }
 
-// silu(g) * u in binary32.
-__device__ __forceinline__ float gate(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
+// silu(g) * u = g u / (1 + e^-g) in binary32.  e^-g = 2^h (1 + l ln 2) with
+// h + l = -g log2 e: h is the rounded product, l its error and the part of
+// log2 e that binary32 drops, so the error of h does not grow with g.  ex2 is
+// within 2 ulp and rcp within 1; with the other roundings the result is within
+// 10 * 2^-24 of |silu(g) u| plus what the arguments' errors make.  Below g =
+// -126 ln 2 rcp flushes its result and silu is 0 (it is above -88 * 2^-126
+// there).
+__device__ __forceinline__ float gate(float g, float u) {
+  constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f;  // log2 e to 48 bits
+  const float c = fminf(fmaxf(g, -88.0f), 88.0f);  // keeps 2^h finite; a NaN comes back in the last line
+  const float h = c * -kLog2e;
+  const float l = fmaf(c, -kLog2eRest, fmaf(c, -kLog2e, -h));
+  float p, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(h));
+  const float t = fmaf(p, l * 0.693147181f, p);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+  return g * r * u;
+}
+
+// The int32 -> binary32 conversion, rounded once, without the conversion unit:
+// the upper 20 bits and the lower 12 become floats by their position in a
+// mantissa (both exact) and one fused multiply-add joins them.
+__device__ __forceinline__ float to_float(int32_t v) {
+  const float hi = __int_as_float((v >> 12) + 0x4B400000) - 12582912.0f;          // 1.5 * 2^23
+  const float lo = __uint_as_float((static_cast<uint32_t>(v) & 0xFFFu) | 0x4B000000u) - 8388608.0f;
+  return fmaf(hi, 4096.0f, lo);
+}
 
 template <int OT>
 __device__ __forceinline__ void store_out(void* Y, int64_t i, float v) {
@@ -293,6 +344,13 @@ struct Epilogue {
     auto z = [](uint32_t acc, float sxv, float swv, float bv) {
       return static_cast<float>(static_cast<int32_t>(acc)) * sxv * swv + bv;
     };
+    // A gated output needs two conversions, an exponential and a reciprocal of
+    // the one unit that does them 16 a clock; half of the conversions go
+    // another way.
+    auto value = [&](uint32_t acc, float sxv, float swv, float bv) {
+      if constexpr (GATED) return to_float(static_cast<int32_t>(acc)) * sxv * swv + bv;
+      return z(acc, sxv, swv, bv);
+    };
 #pragma unroll
     for (int i = 0; i < CHUNK / 8; ++i) {  // 8 tokens each
       const float2 s = *reinterpret_cast<const float2*>(sx + 8 * i + col);
@@ -301,7 +359,7 @@ struct Epilogue {
       for (int h = 0; h < 2; ++h) {
         const float sv = h ? s.y : s.x;
         const float z0 = z(lo[4 * i + h], sv, sw[0], b[0]), z1 = z(lo[4 * i + 2 + h], sv, sw[1], b[1]);
-        const float z2 = z(hi[4 * i + h], sv, sw[2], b[2]), z3 = z(hi[4 * i + 2 + h], sv, sw[3], b[3]);
+        const float z2 = value(hi[4 * i + h], sv, sw[2], b[2]), z3 = value(hi[4 * i + 2 + h], sv, sw[3], b[3]);
         if constexpr (GATED) {
           y[0][h] = gate(z0, z2);
           y[1][h] = gate(z1, z3);
@@ -433,8 +491,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   // and so may the weights (a user may have quantised them just now): nothing
   // is read before that kernel is done.  Only then may the next one start, so
   // that a kernel two calls later never runs beside one two calls earlier.
-  pdl_wait();
-  pdl_launch_dependents();
+  // Without offsets the tiles are known before, and the wait comes after them.
+  auto previous_done = [&]() {
+    pdl_wait();
+    pdl_launch_dependents();
+  };
+  const bool ragged = p.offsets != nullptr;
+  if (ragged) previous_done();
   if (warp == 2) scan_groups(p, groups);
   __syncthreads();
   tc_fence_after();
@@ -451,18 +514,27 @@ __global__ void __launch_bounds__(THREADS, 1)
     // then uniform values.  (With the loop inside `if (lane == 0)` an MMA took
     // 71 cycles to issue and a stage 300 more, whatever its size.)
     const bool issuer = elect_one();
-    int it = 0, s = 0;      // stages filled so far; the stage to fill next
+    int s = 0;              // the stage to fill next
     uint32_t phase = 1;     // parity its `empty` barrier had before this round (passes at once in round 0)
     bool ok = true;
-    for (Walk t(p, groups, unit, units); ok && t.more(); t.next(p, groups)) {
-      const int cols = (t.tokens() + 15) / 16 * 16;  // MMA N
-      const int mine = cols / 2;                     // token rows this CTA copies
-      const int x0 = t.row() + rank * mine;
-      const int quarters = quarters_of(p, mine);
-      const CUtensorMap* tmap_x = &tmaps_x.m[quarters - 1];
-      const int wt = 2 * t.nt + rank;  // this CTA's weight rows, in units of H
-      const uint32_t tx = static_cast<uint32_t>(2 * p.KPB * (a_bytes + quarters * p.quarter * BK));
-      for (int u = 0; u < p.NU; ++u, ++it) {
+    // The next tile is worked out while this one's first stages are on their
+    // way (between two tiles it left the tensor cores idle for 1200 cycles).
+    struct Copies {
+      int g, wt, x0, quarters;  // group, weight rows in units of H, first token row and height
+    };
+    auto copies = [&](const Walk& t) {
+      const int mine = (t.tokens() + 15) / 16 * 8;  // token rows this CTA copies: half the MMA's N
+      return Copies{t.g, 2 * t.nt + rank, t.row() + rank * mine, quarters_of(p, mine)};
+    };
+    Walk t(p, groups, unit, units);
+    Copies next{};
+    if (t.more()) next = copies(t);
+    if (!ragged) previous_done();
+    for (bool more = t.more(); ok && more;) {
+      const Copies c = next;
+      const CUtensorMap* tmap_x = &tmaps_x.m[c.quarters - 1];
+      const uint32_t tx = static_cast<uint32_t>(2 * p.KPB * (a_bytes + c.quarters * p.quarter * BK));
+      for (int u = 0; u < p.NU; ++u) {
         ok = mbar_wait_stage(&empty[s], phase, p.wait_ns, kErrTimeoutProducer);
         if (!ok) break;
         if (issuer) {
@@ -470,10 +542,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t bar = map_shared_rank(&full[s], 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
           if constexpr (GATED)
-            tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.g, wt * (p.H / 32), kb);
+            tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * c.g, c.wt * (p.H / 32), kb);
           else
-            tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.g);
-          tma_load_3d_pair(stage_b(s), tmap_x, bar, x, x0, kb);
+            tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, c.wt * p.H, kb, c.g);
+          tma_load_3d_pair(stage_b(s), tmap_x, bar, x, c.x0, kb);
+        }
+        if (u == 0) {
+          t.next(p, groups);
+          more = t.more();
+          if (more) next = copies(t);
         }
         if (++s == p.stages) {
           s = 0;
@@ -486,13 +563,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const bool issuer = elect_one();
+    if (!ragged) previous_done();
     if (rank == 0) {
       const uint32_t ring = smem_addr(smem);
       int s = 0, tc = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (Walk t(p, groups, unit, units); ok && t.more(); t.next(p, groups), ++tc) {
-        const int cols = (t.tokens() + 15) / 16 * 16;
+      Walk t(p, groups, unit, units);
+      int next = t.more() ? (t.tokens() + 15) / 16 * 16 : 0;
+      for (; ok && next; ++tc) {
+        const int cols = next;
         const uint32_t idesc = idesc_i8_s32(2 * BM, cols);
         // k-blocks of a stage lie as the copy put them: its rows apart
         const uint32_t b_step = static_cast<uint32_t>(quarters_of(p, cols / 2) * p.quarter * BK) >> 4;
@@ -517,6 +597,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int k = 1; k < BK / 32; ++k) mma_i8_low_pair(d, alow + 2 * k, blow + 2 * k, idesc, 1u);
             }
             mma_commit_pair(&empty[s], 0x3);
+          }
+          if (u == 0) {
+            t.next(p, groups);
+            next = t.more() ? (t.tokens() + 15) / 16 * 16 : 0;
           }
           if (++s == p.stages) {
             s = 0;
@@ -568,6 +652,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     static_assert(32 * EPI_WARPS >= MAX_BT, "a thread for each token's scale");
     int tc = 0;
     Walk t(p, groups, unit, units);
+    if (!ragged) previous_done();
     Ahead next;
     if (t.more()) next = fetch(t);
     for (; t.more(); ++tc) {

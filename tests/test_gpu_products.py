@@ -4,8 +4,8 @@ expert positions and combine, each against its definition in 64 bits.
 Tolerances count the kernels' roundings.  u = 2^-24 is half a step of binary32, eps(t) / 2 half a step of the output
 type.  The int32 sums are exact.
   z = fl(fl(fl(acc) sx) sw) [+ b]: at most 3 u |z0| before the bias (second-order terms: 3.1 u), u |z| for the addition;
-  gate: with dg, du the errors of its arguments, |silu'| < 1.1, and exp within 2 ulp (2^-22), one addition, one division
-  and one product: dy <= 1.1 dg |u| + |silu(g)| du + (2^-22 + 4 u) |y|;
+  gate: with dg, du the errors of its arguments, |silu'| < 1.1; 2^h within 2 ulp (4 u), its correction, 1 + t, the
+  reciprocal (1 ulp, 2 u) and two products one rounding each: dy <= 1.1 dg |u| + |silu(g)| du + 10 u |y|;
   the output's own rounding: eps / 2 |y|, or half the smallest subnormal step.
 """
 import numpy as np
@@ -62,7 +62,7 @@ def expected(Xq, sx, Wq, sw, b, gated, dtype):
         g, u, dg, du = z[:, :F], z[:, F:], dz[:, :F], dz[:, F:]
         s = g * torch.sigmoid(g)
         y = s * u
-        dy = 1.1 * dg * u.abs() + s.abs() * du + (2.0 ** -22 + 4 * U) * y.abs()
+        dy = 1.1 * dg * u.abs() + s.abs() * du + 10 * U * y.abs()
     return y, dy + torch.finfo(dtype).eps / 2 * y.abs() * (1 + 2.0 ** -8) + HALF_SUBNORMAL[dtype]
 
 
@@ -162,6 +162,30 @@ def test_gate_at_large_arguments(L):
     Y = L.llmint8_scaled_matmul(Xq, one[:1].contiguous(), Wq, one, gated=True, dtype=torch.float32)[0]
     z = float(K * 127 * 127)
     assert (Y[0::2] == z * z).all() and (Y[1::2] == 0).all()
+
+
+def test_gate_over_its_whole_range(L):
+    """silu at arguments from the smallest to the largest magnitude, infinite and NaN ones: the bound of the gate's
+    own roundings, 0 where its value is above -88 * 2^-126, NaN where the formula has it."""
+    g = torch.cat([torch.linspace(-90, 90, 20001), torch.logspace(-38, 38, 2001), -torch.logspace(-38, 38, 2001),
+                   torch.tensor([0.0, 3.4e38, -3.4e38, float("inf"), float("nan")])]).float().cuda()
+    T = g.numel()
+    Xq = torch.zeros(T, 16, dtype=torch.int8, device="cuda")
+    Xq[:, 0] = 1
+    Wq = torch.zeros(32, 16, dtype=torch.int8, device="cuda")
+    Wq[:16, 0], sw = 1, torch.ones(32, device="cuda")
+    b = torch.cat([torch.zeros(16), torch.full((16,), 3.0)]).cuda()
+    Y = L.llmint8_scaled_matmul(Xq, g, Wq, sw, bias=b, gated=True, dtype=torch.float32)[:, 0]
+    d = g.double()
+    y = 3 * d * torch.sigmoid(d)
+    # The reciprocal is flushed where 1 + e^-g > 2^126, that is g < -126 ln 2 = -87.3365; at and below -87.33 the
+    # value itself is at most 87.33 e^-87.33 = 87.9 * 2^-126 (|g| e^g falls as g does), flushed or not.
+    small = (d < -87.33) & (d.isfinite())
+    assert (Y[small].abs() <= 3 * 88 * 2.0 ** -126).all()
+    assert Y[-2].isnan() and Y[-1].isnan()      # an infinite scale: the value channel's sum is 0 * inf
+    rest = ~small & d.isfinite() & (y.abs() <= 3.4e38)
+    check(Y[rest], y[rest], 11 * U * y[rest].abs() + 2.0 ** -126)
+    assert (Y[d.isfinite() & (y > 3.41e38)] == float("inf")).all()
 
 
 # ------------------------------------------------------------------ grouped product

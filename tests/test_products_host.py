@@ -122,6 +122,37 @@ def scan_groups(offsets, S, BT, nN):
     return off, cum, bad
 
 
+def token_tiles(m, BT):
+    """ceil(m / BT) by a multiplication, as the kernel takes it."""
+    shift = 31 + (BT - 1).bit_length()
+    product = (m + BT - 1) * ((1 << shift) // BT + 1)
+    assert product < 1 << 64
+    return product >> shift
+
+
+def tile_rows(m, mt, BT):
+    if mt <= 1:
+        return (m + 15) // 16 * 16
+    share = int(np.float32(m) / np.float32(mt)) + 1
+    per = min((share + 15) // 16 * 16, BT)
+    return per + 16 if per * mt < m else per
+
+
+@pytest.mark.parametrize("BT", range(16, 257, 16))
+def test_tile_arithmetic(BT):
+    """The quotient without a division is exact up to the largest m, and the tiles of a group cover it: equal to the
+    rounding, none empty, none above BT."""
+    rng = np.random.default_rng(BT)
+    ms = np.concatenate([np.arange(1, 5000), rng.integers(1, 2 ** 31 - 256, 2000),
+                         2 ** 31 - 256 - np.arange(600), (rng.integers(1, 2 ** 22, 500) * BT)[:, None].repeat(3, 1).ravel()
+                         + np.tile([-1, 0, 1], 500)])
+    for m in ms[ms <= 2 ** 31 - 256].tolist():
+        mt = token_tiles(m, BT)
+        assert mt == -(-m // BT)
+        per = tile_rows(m, mt, BT)
+        assert per % 16 == 0 and 16 <= per <= BT and per * mt >= m and per * (mt - 1) < m
+
+
 def find_tile(off, cum, BT, w):
     lo, hi = 0, len(cum) - 1
     while hi - lo > 1:
@@ -129,7 +160,8 @@ def find_tile(off, cum, BT, w):
         lo, hi = (mid, hi) if cum[mid] <= w else (lo, mid)
     begin, m = off[lo], off[lo + 1] - off[lo]
     mt = -(-m // BT)
-    per = -(-(-(-m // mt)) // 16) * 16
+    assert mt == token_tiles(m, BT)
+    per = tile_rows(m, mt, BT)
     r = w - cum[lo]
     nt, i = r // mt, r % mt
     return lo, begin + i * per, min(per, m - i * per), nt
