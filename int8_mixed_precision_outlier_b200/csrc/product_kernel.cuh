@@ -21,7 +21,7 @@
 // unit, + units, ...; tile w belongs to the group whose cumulative tile count covers it, found in
 // shared memory from the device's offsets (the host never waits for them).
 // Warp 0 copies (TMA, 128-byte swizzle), warp 1 issues tcgen05.mma kind::i8
-// and owns TMEM, warps 2-17 write the results.  Two 256-column accumulators
+// and owns TMEM, warps 2-17 write the results, warp 18 plans the tiles.  Two 256-column accumulators
 // let the next tile's products run while the epilogue drains the last one.
 // Every mbarrier wait is bounded.
 #pragma once
@@ -39,7 +39,9 @@ constexpr int KPB_MAX = 4;         // k-blocks per stage
 constexpr int MAX_STAGES = 12;
 constexpr int MAX_GROUPS = 1024;
 constexpr int EPI_WARPS = 16;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int PLAN_WARP = 2 + EPI_WARPS;
+constexpr int THREADS = 32 * (PLAN_WARP + 1);
+constexpr int AHEAD = 8;           // tiles that the planning warp may be ahead of the slowest reader
 constexpr int TMEM_COLS = 512;     // two accumulators of MAX_BT columns
 constexpr int RING_BYTES = 192 * 1024;  // stages, and 16 KiB past the last one (see SLACK)
 // Behind the ring: the epilogue's staging.  A tile of fewer than 128 weight
@@ -49,10 +51,13 @@ constexpr int STAGING_BYTES = 1024;  // of one epilogue warp
 constexpr int SLACK_BYTES = EPI_WARPS * STAGING_BYTES;
 static_assert(SLACK_BYTES >= BM * BK, "the last stage's 128 rows end inside shared memory");
 constexpr int SX_BYTES = 2 * MAX_BT * 4;
-constexpr int GROUP_BYTES = 2 * (MAX_GROUPS + 1) * 4 + MAX_GROUPS * 4 + MAX_GROUPS * 2;
-constexpr int BAR_BYTES = 512;
+constexpr int GROUP_BYTES = (2 * (MAX_GROUPS + 1) * 4 + MAX_GROUPS * 4 + MAX_GROUPS * 2 + 15) / 16 * 16;
+constexpr int BAR_BYTES = 512;     // barriers, and behind them the tile ring
+constexpr int TILES_AT = 384;
+static_assert((2 * MAX_STAGES + 5 + 2 * AHEAD) * 8 + 4 <= TILES_AT && TILES_AT + 16 * AHEAD <= BAR_BYTES, "layout");
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + SLACK_BYTES + SX_BYTES + GROUP_BYTES + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+static_assert((RING_BYTES + SLACK_BYTES + SX_BYTES + GROUP_BYTES + TILES_AT) % 16 == 0, "the tile ring holds int4");
 
 enum : int { kF16 = 0, kBF16 = 1, kF32 = 2 };
 
@@ -457,7 +462,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* tfull = empty + MAX_STAGES;  // [2]
   uint64_t* tempty = tfull + 2;          // [2]
   uint64_t* done = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* planned = done + 1;          // [AHEAD]: a tile is in the ring
+  uint64_t* taken = planned + AHEAD;     // [AHEAD]: every reader has it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(taken + AHEAD);
+  int4* tiles = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(full) + TILES_AT);  // [AHEAD]
 
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
@@ -477,6 +485,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&tempty[b], 2 * EPI_WARPS);
     }
     mbar_init(done, 1);
+    for (int i = 0; i < AHEAD; ++i) {
+      mbar_init(&planned[i], 1);
+      mbar_init(&taken[i], 1 + (rank == 0 ? 1 : 0) + EPI_WARPS);  // producer, MMA issuer, epilogue warps
+    }
     fence_barrier_init();
   }
   __syncwarp();
@@ -491,15 +503,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   // and so may the weights (a user may have quantised them just now): nothing
   // is read before that kernel is done.  Only then may the next one start, so
   // that a kernel two calls later never runs beside one two calls earlier.
-  // Without offsets the tiles are known before, and the wait comes after them.
   auto previous_done = [&]() {
     pdl_wait();
     pdl_launch_dependents();
   };
-  const bool ragged = p.offsets != nullptr;
-  if (ragged) previous_done();
-  if (warp == 2) scan_groups(p, groups);
-  __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int a_bytes = p.H * BK;                     // of one k-block
@@ -508,32 +515,71 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto stage_b = [&](int s) { return smem + s * stage_bytes; };
   auto stage_a = [&](int s) { return smem + s * stage_bytes + p.KPB * b_bytes; };
 
-  if (warp == 0) {
+  // A wait of a whole warp with one outcome: lanes that gave up and lanes that
+  // did not would part, and never meet again at a warp-wide step.  (The loops
+  // over the stages have no such step and vote once a tile.)
+  auto all_wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+    return __all_sync(0xffffffffu, mbar_wait_stage(bar, parity, p.wait_ns, code)) != 0;
+  };
+
+  // The next tile of the ring, for a reader that has had `i` of them: false at
+  // the end (or when the wait ran out).
+  struct Tile {
+    int g, nt, row, tokens;  // group, tile along the channels, first row of Xq / Y, rows
+  };
+  auto take = [&](int& i, Tile& t) {
+    const int slot = i % AHEAD;
+    const bool ok = all_wait(&planned[slot], (i / AHEAD) & 1, kErrTimeoutProducer);
+    const int4 v = tiles[slot];
+    t = Tile{v.x, v.y, v.z, v.w};
+    __syncwarp();  // all lanes have read
+    if (lane == 0) mbar_arrive(&taken[slot]);
+    ++i;
+    return ok && t.g >= 0;
+  };
+
+  if (warp == PLAN_WARP) {
+    // ------------------------------------------------------------ tile plan
+    // One warp works the tiles out ahead of the others.  (With a walk in every
+    // role the next tile took the MMA issuer about 1000 cycles, beside the
+    // epilogue's warps, with two MMAs in flight.)
+    const bool ragged = p.offsets != nullptr;
+    if (ragged) previous_done();
+    scan_groups(p, groups);
+    __syncwarp();
+    Walk t(p, groups, unit, units);
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const int slot = i % AHEAD;
+      ok = i < AHEAD || all_wait(&taken[slot], ((i / AHEAD) & 1) ^ 1, kErrTimeoutProducer);
+      const bool more = ok && t.more();
+      if (lane == 0) {
+        tiles[slot] = more ? make_int4(t.g, t.nt, t.row(), t.tokens()) : make_int4(-1, 0, 0, 0);
+        mbar_arrive(&planned[slot]);
+      }
+      __syncwarp();
+      if (!more) break;
+      if (i == 0 && !ragged) previous_done();  // without offsets nothing here waits for it
+      t.next(p, groups);
+    }
+  } else if (warp == 0) {
     // ------------------------------------------------------------ producer
     // All lanes walk the loop, one issues: its addresses and coordinates are
     // then uniform values.  (With the loop inside `if (lane == 0)` an MMA took
     // 71 cycles to issue and a stage 300 more, whatever its size.)
     const bool issuer = elect_one();
+    previous_done();
     int s = 0;              // the stage to fill next
     uint32_t phase = 1;     // parity its `empty` barrier had before this round (passes at once in round 0)
     bool ok = true;
-    // The next tile is worked out while this one's first stages are on their
-    // way (between two tiles it left the tensor cores idle for 1200 cycles).
-    struct Copies {
-      int g, wt, x0, quarters;  // group, weight rows in units of H, first token row and height
-    };
-    auto copies = [&](const Walk& t) {
-      const int mine = (t.tokens() + 15) / 16 * 8;  // token rows this CTA copies: half the MMA's N
-      return Copies{t.g, 2 * t.nt + rank, t.row() + rank * mine, quarters_of(p, mine)};
-    };
-    Walk t(p, groups, unit, units);
-    Copies next{};
-    if (t.more()) next = copies(t);
-    if (!ragged) previous_done();
-    for (bool more = t.more(); ok && more;) {
-      const Copies c = next;
-      const CUtensorMap* tmap_x = &tmaps_x.m[c.quarters - 1];
-      const uint32_t tx = static_cast<uint32_t>(2 * p.KPB * (a_bytes + c.quarters * p.quarter * BK));
+    int i = 0;
+    for (Tile t; ok && take(i, t);) {
+      const int mine = (t.tokens + 15) / 16 * 8;  // token rows this CTA copies: half the MMA's N
+      const int wt = 2 * t.nt + rank;             // this CTA's weight rows, in units of H
+      const int x0 = t.row + rank * mine;
+      const int quarters = quarters_of(p, mine);
+      const CUtensorMap* tmap_x = &tmaps_x.m[quarters - 1];
+      const uint32_t tx = static_cast<uint32_t>(2 * p.KPB * (a_bytes + quarters * p.quarter * BK));
       for (int u = 0; u < p.NU; ++u) {
         ok = mbar_wait_stage(&empty[s], phase, p.wait_ns, kErrTimeoutProducer);
         if (!ok) break;
@@ -542,78 +588,76 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t bar = map_shared_rank(&full[s], 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
           if constexpr (GATED)
-            tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * c.g, c.wt * (p.H / 32), kb);
+            tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.g, wt * (p.H / 32), kb);
           else
-            tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, c.wt * p.H, kb, c.g);
-          tma_load_3d_pair(stage_b(s), tmap_x, bar, x, c.x0, kb);
-        }
-        if (u == 0) {
-          t.next(p, groups);
-          more = t.more();
-          if (more) next = copies(t);
+            tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.g);
+          tma_load_3d_pair(stage_b(s), tmap_x, bar, x, x0, kb);
         }
         if (++s == p.stages) {
           s = 0;
           phase ^= 1;
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
     }
     // Every copy of both CTAs has landed once the MMAs that read it are done:
     // the `done` commit covers that.
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const bool issuer = elect_one();
-    if (!ragged) previous_done();
+    previous_done();
     if (rank == 0) {
-      const uint32_t ring = smem_addr(smem);
+      const uint32_t ring = sdesc_low(smem_addr(smem)), stage_step = static_cast<uint32_t>(stage_bytes) >> 4;
+      const uint32_t a_at = static_cast<uint32_t>(p.KPB * b_bytes) >> 4, a_step = static_cast<uint32_t>(a_bytes) >> 4;
       int s = 0, tc = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      Walk t(p, groups, unit, units);
-      int next = t.more() ? (t.tokens() + 15) / 16 * 16 : 0;
-      for (; ok && next; ++tc) {
-        const int cols = next;
+      uint32_t phase = 0, stage = ring;  // `stage`: descriptor of the stage's token rows
+      bool ok = true, ready = false;
+      int i = 0;
+      for (Tile t; ok && take(i, t); ++tc) {
+        const int cols = (t.tokens + 15) / 16 * 16;
         const uint32_t idesc = idesc_i8_s32(2 * BM, cols);
         // k-blocks of a stage lie as the copy put them: its rows apart
         const uint32_t b_step = static_cast<uint32_t>(quarters_of(p, cols / 2) * p.quarter * BK) >> 4;
+        uint32_t add = 0;  // the tile's first product overwrites the accumulator
         const int buf = tc & 1;
         if (tc >= 2) {
-          ok = mbar_wait_stage<true>(&tempty[buf], ((tc >> 1) - 1) & 1, p.wait_ns, kErrTimeoutMma);
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_stage<true>(&tempty[buf], ((tc >> 1) - 1) & 1, p.wait_ns, kErrTimeoutMma));
           if (!ok) break;
         }
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(buf * MAX_BT);
         for (int u = 0; u < p.NU; ++u) {
-          ok = mbar_wait_stage(&full[s], phase, p.wait_ns, kErrTimeoutMma);
+          if (!ready) ok = mbar_wait_stage(&full[s], phase, p.wait_ns, kErrTimeoutMma);
           if (!ok) break;
-          tc_fence_after();
-          if (issuer) {
-            const int nkb = min(p.KPB, p.KB - u * p.KPB);
-            uint32_t blow = sdesc_low(ring + s * stage_bytes);
-            uint32_t alow = sdesc_low(ring + s * stage_bytes + p.KPB * b_bytes);
-            for (int j = 0; j < nkb; ++j, alow += a_bytes >> 4, blow += b_step) {
-              mma_i8_low_pair(d, alow, blow, idesc, (u > 0 || j > 0) ? 1u : 0u);
-#pragma unroll
-              for (int k = 1; k < BK / 32; ++k) mma_i8_low_pair(d, alow + 2 * k, blow + 2 * k, idesc, 1u);
-            }
-            mma_commit_pair(&empty[s], 0x3);
-          }
-          if (u == 0) {
-            t.next(p, groups);
-            next = t.more() ? (t.tokens() + 15) / 16 * 16 : 0;
-          }
+          uint64_t* const freed = &empty[s];
+          const uint32_t here = stage;
+          stage += stage_step;
           if (++s == p.stages) {
             s = 0;
+            stage = ring;
             phase ^= 1;
           }
+          // Asked now, answered while the products are issued.
+          ready = mbar_ready(&full[s], phase);
+          tc_fence_after();
+          if (issuer) {
+            const int nkb = u + 1 < p.NU ? p.KPB : p.KB - u * p.KPB;
+            uint32_t blow = here, alow = here + a_at;
+            for (int j = 0; j < nkb; ++j, alow += a_step, blow += b_step) {
+#pragma unroll
+              for (int k = 0; k < BK / 32; ++k) {
+                mma_i8_low_pair(d, alow + 2 * k, blow + 2 * k, idesc, add);
+                add = 1;
+              }
+            }
+            mma_commit_pair(freed, 0x3);
+          }
         }
-        if (ok && issuer) {
-          mma_commit_pair(&tfull[buf], 0x3);
-        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && issuer) mma_commit_pair(&tfull[buf], 0x3);
       }
-      if (issuer) {
-        mma_commit_pair(done, 0x3);
-      }
+      if (issuer) mma_commit_pair(done, 0x3);
     }
     // The MMAs (of both CTAs) are complete before TMEM is released.
     mbar_wait_stage(done, 0, p.wait_ns, kErrTimeoutMma);
@@ -633,10 +677,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       int m0, tok, c, n;  // rows of Y; this warp's channels: n from c on inside Y and the tile
       float sx, sw[4], b[4];
     };
-    auto fetch = [&](const Walk& t) {
+    auto fetch = [&](const Tile& t) {
       Ahead a;
-      a.m0 = t.row();
-      a.tok = t.tokens();
+      a.m0 = t.row;
+      a.tok = t.tokens;
       a.c = (2 * t.nt + rank) * tile_ch + q * Epi::CH;
       a.n = min(min(tile_ch - q * Epi::CH, Epi::CH), p.No - a.c);
       a.sx = etid < a.tok ? p.sx[a.m0 + etid] : 0.0f;
@@ -650,23 +694,27 @@ __global__ void __launch_bounds__(THREADS, 1)
       return a;
     };
     static_assert(32 * EPI_WARPS >= MAX_BT, "a thread for each token's scale");
-    int tc = 0;
-    Walk t(p, groups, unit, units);
-    if (!ragged) previous_done();
-    Ahead next;
-    if (t.more()) next = fetch(t);
-    for (; t.more(); ++tc) {
+    previous_done();
+    int tc = 0, i = 0;
+    Tile t;
+    Ahead next{};
+    bool more = take(i, t);
+    if (more) next = fetch(t);
+    // All epilogue threads leave together, at the barrier: after the last tile,
+    // or when a wait of any of them ran out.
+    for (;; ++tc) {
       const Ahead a = next;
       const int buf = tc & 1;
       float* sxb = sx_s + buf * MAX_BT;
       // The buffer's readers two tiles ago are past the previous tile's barrier.
-      if (etid < a.tok) sxb[etid] = a.sx;
+      if (more && etid < a.tok) sxb[etid] = a.sx;
       // One thread polls, the others sleep at the barrier.
-      const bool ok = etid != 0 || mbar_wait_stage(&tfull[buf], (tc >> 1) & 1, p.wait_ns, kErrTimeoutEpilogue);
+      const bool ok =
+          more && (etid != 0 || mbar_wait_stage(&tfull[buf], (tc >> 1) & 1, p.wait_ns, kErrTimeoutEpilogue));
       if (!named_barrier_and(1, 32 * EPI_WARPS, ok)) break;  // also: sxb is written
       tc_fence_after();
-      t.next(p, groups);
-      if (t.more()) next = fetch(t);
+      more = take(i, t);
+      if (more) next = fetch(t);
       const uint32_t addr =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * MAX_BT);
       if (a.n > 0) {

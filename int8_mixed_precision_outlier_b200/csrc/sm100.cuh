@@ -114,6 +114,18 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
         : "memory");
   return done != 0;
 }
+// Whether the phase has completed, without waiting at all (try_wait may sleep).
+__device__ __forceinline__ bool mbar_ready(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_stage(uint64_t* bar, uint32_t parity, uint64_t limit_ns, uint32_t code) {
   uint64_t t0 = 0;
