@@ -43,21 +43,19 @@ constexpr int PLAN_WARP = 2 + EPI_WARPS;
 constexpr int THREADS = 32 * (PLAN_WARP + 1);
 constexpr int AHEAD = 8;           // tiles that the planning warp may be ahead of the slowest reader
 constexpr int TMEM_COLS = 512;     // two accumulators of MAX_BT columns
-constexpr int RING_BYTES = 192 * 1024;  // stages, and 16 KiB past the last one (see SLACK)
-// Behind the ring: the epilogue's staging.  A tile of fewer than 128 weight
-// rows is multiplied as 128, and the lanes past its end (never stored) read
-// whatever follows in shared memory: after the last stage, these 16 KiB.
-constexpr int STAGING_BYTES = 1024;  // of one epilogue warp
-constexpr int SLACK_BYTES = EPI_WARPS * STAGING_BYTES;
-static_assert(SLACK_BYTES >= BM * BK, "the last stage's 128 rows end inside shared memory");
+constexpr int RING_BYTES = 208 * 1024;
 constexpr int SX_BYTES = 2 * MAX_BT * 4;
 constexpr int GROUP_BYTES = (2 * (MAX_GROUPS + 1) * 4 + MAX_GROUPS * 4 + MAX_GROUPS * 2 + 15) / 16 * 16;
 constexpr int BAR_BYTES = 512;     // barriers, and behind them the tile ring
 constexpr int TILES_AT = 384;
 static_assert((2 * MAX_STAGES + 5 + 2 * AHEAD) * 8 + 4 <= TILES_AT && TILES_AT + 16 * AHEAD <= BAR_BYTES, "layout");
-constexpr int SMEM_BYTES = 1024 + RING_BYTES + SLACK_BYTES + SX_BYTES + GROUP_BYTES + BAR_BYTES;
+constexpr int SMEM_BYTES = 1024 + RING_BYTES + SX_BYTES + GROUP_BYTES + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-static_assert((RING_BYTES + SLACK_BYTES + SX_BYTES + GROUP_BYTES + TILES_AT) % 16 == 0, "the tile ring holds int4");
+static_assert((RING_BYTES + SX_BYTES + GROUP_BYTES + TILES_AT) % 16 == 0, "the tile ring holds int4");
+// A tile of fewer than 128 weight rows is multiplied as 128: the lanes past its
+// end, which are never stored, read whatever follows in shared memory, after
+// the last stage these tables.
+static_assert(SX_BYTES + GROUP_BYTES + BAR_BYTES >= BM * BK, "the last stage's 128 rows end inside shared memory");
 
 enum : int { kF16 = 0, kBF16 = 1, kF32 = 2 };
 
@@ -306,122 +304,53 @@ __device__ __forceinline__ uint32_t pack_two(float a, float b) {
 
 // ------------------------------------------------------------ epilogue
 // The accumulator has channels along the TMEM lanes and tokens along the
-// columns; Y has channels along its rows.  A warp turns CHUNK tokens by the
-// channels of its 32 lanes around through its own 1 KiB of shared memory, so
-// that Y is written 16 bytes a thread, 32 to 128 bytes of a row at a time, and
-// no warp waits for another.
+// columns: a lane of a warp holds one channel, and a warp writes 32
+// consecutive channels of a token (gated: 16 channels of two tokens) straight
+// from its registers.  Shared memory stays out of it: the products read and
+// the copies write about all that it can move, and turning the tile around in
+// it (for 16 bytes a thread) slowed them down by a quarter of a K = 2048 tile.
 //
-// tcgen05.ld 16x256b gives a thread two tokens of one channel per register
-// pair: the shape that stmatrix.trans stores 8 channels of a token from.  In
-// a gated tile TMEM lanes 0-15 of a quadrant hold the gates and lanes 16-31 the
-// values of the same 16 channels, so both halves of an output meet in a thread.
+// In a gated tile lanes 0-15 of a quadrant hold the gates and lanes 16-31 the
+// values of the same 16 channels.  Of two tokens, lanes 0-15 take the first:
+// they give their gate of the second for the value of the first.
 template <bool GATED, int OT>
 struct Epilogue {
-  static constexpr bool k32 = OT == kF32;
-  static constexpr int SIZE = k32 ? 4 : 2;
-  static constexpr int CH = GATED ? 16 : 32;                 // channels of a warp
-  static constexpr int CHUNK = STAGING_BYTES / (CH * SIZE);  // tokens staged at a time: 8, 16 or 32
-  static constexpr int VEC = 16 / SIZE;                      // elements in 16 bytes
+  static constexpr int CH = GATED ? 16 : 32;  // channels of a warp
+  static constexpr int CHUNK = 32;            // tokens at a time
 
-  // Byte offset of a token's channel in the staging, [token][channel] with the
-  // 16-byte pieces (binary32: pairs of pieces) of each 128 bytes permuted so
-  // that neither the writes nor the reads meet in a bank.
-  __device__ static uint32_t at(int token, int channel) {
-    const int byte = (token * CH + channel) * SIZE;
-    if constexpr (k32) return byte ^ (((token >> 1) & 3) << 5);
-    if constexpr (!k32 && !GATED) return byte ^ (((token >> 1) & 3) << 4);
-    return byte ^ (((token >> 2) & 1) << 4);
-  }
-
-  // Outputs of CHUNK columns, staged by this warp.  `sw`, `b`: of TMEM lanes
-  // l / 4 + {0, 8, 16, 24} of the quadrant.
-  __device__ static void stage(uint8_t* st, uint32_t addr, int lane, const float* sx, const float (&sw)[4],
-                               const float (&b)[4]) {
-    uint32_t lo[CHUNK / 2], hi[CHUNK / 2];  // TMEM lanes 0-15 and 16-31
-    [[maybe_unused]] uint32_t keep0 = 0, keep1 = 0;
-    tmem_ld_16lanes(addr, lo);
-    tmem_ld_16lanes(addr + (16u << 16), hi);
-    tmem_ld_wait();
-    tmem_regs_ready(lo);
-    tmem_regs_ready(hi);
-    const int r = lane >> 2, col = 2 * (lane & 3);
-    const int m = lane >> 3, j = lane & 7;  // stmatrix: matrix and token of this lane's address
-    auto z = [](uint32_t acc, float sxv, float swv, float bv) {
-      return static_cast<float>(static_cast<int32_t>(acc)) * sxv * swv + bv;
-    };
-    // A gated output needs two conversions, an exponential and a reciprocal of
-    // the one unit that does them 16 a clock; half of the conversions go
-    // another way.
-    auto value = [&](uint32_t acc, float sxv, float swv, float bv) {
-      if constexpr (GATED) return to_float(static_cast<int32_t>(acc)) * sxv * swv + bv;
-      return z(acc, sxv, swv, bv);
-    };
+  // Tokens 0 .. cnt - 1 of CHUNK columns; `y`: this lane's channel in the first
+  // token's row of Y (gated: in the row of the token it takes first).
+  template <bool FULL>
+  __device__ static void write(const uint32_t (&r)[CHUNK], const float* sx, float sw, float b, bool mine, int cnt,
+                               int lane, uint8_t* y, int64_t row_bytes) {
+    const bool upper = lane >= 16;
 #pragma unroll
-    for (int i = 0; i < CHUNK / 8; ++i) {  // 8 tokens each
-      const float2 s = *reinterpret_cast<const float2*>(sx + 8 * i + col);
-      float y[4][2];  // [channel block of 8][token]
+    for (int j0 = 0; j0 < CHUNK; j0 += 4) {
+      if (!FULL && j0 >= cnt) break;
+      const float4 s4 = *reinterpret_cast<const float4*>(sx + j0);
+      const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+      float z[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float sv = h ? s.y : s.x;
-        const float z0 = z(lo[4 * i + h], sv, sw[0], b[0]), z1 = z(lo[4 * i + 2 + h], sv, sw[1], b[1]);
-        const float z2 = value(hi[4 * i + h], sv, sw[2], b[2]), z3 = value(hi[4 * i + 2 + h], sv, sw[3], b[3]);
-        if constexpr (GATED) {
-          y[0][h] = gate(z0, z2);
-          y[1][h] = gate(z1, z3);
-        } else {
-          y[0][h] = z0;
-          y[1][h] = z1;
-          y[2][h] = z2;
-          y[3][h] = z3;
-        }
+      for (int i = 0; i < 4; ++i) {
+        // A gated output takes two conversions, an exponential and a reciprocal
+        // of the one unit that does them 16 a clock: half of the conversions go
+        // another way.
+        const int32_t acc = static_cast<int32_t>(r[j0 + i]);
+        z[i] = (GATED && (i & 1) ? to_float(acc) : static_cast<float>(acc)) * sv[i] * sw + b;
       }
-      if constexpr (k32) {
+      if constexpr (GATED) {
 #pragma unroll
-        for (int c = 0; c < CH / 8; ++c)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float*>(st + at(8 * i + col + h, c * 8 + r)) = y[c][h];
-      } else if constexpr (GATED) {
-        // two channel blocks of 8 tokens; the other two matrices are the next
-        // 8 tokens', so these wait for them
-        if (i & 1) {
-          stmatrix_x4_trans(smem_addr(st) + at(8 * (i - 1 + (m >> 1)) + j, (m & 1) * 8), keep0, keep1,
-                            pack_two<OT>(y[0][0], y[0][1]), pack_two<OT>(y[1][0], y[1][1]));
-        } else {
-          keep0 = pack_two<OT>(y[0][0], y[0][1]);
-          keep1 = pack_two<OT>(y[1][0], y[1][1]);
+        for (int i = 0; i < 4; i += 2) {
+          const float other = __shfl_xor_sync(0xffffffffu, upper ? z[i] : z[i + 1], 16);
+          const float v = gate(upper ? other : z[i], upper ? z[i + 1] : other);
+          if (mine && (FULL || j0 + i + (upper ? 1 : 0) < cnt)) store_out<OT>(y, 0, v);
+          y += 2 * row_bytes;
         }
       } else {
-        stmatrix_x4_trans(smem_addr(st) + at(8 * i + j, m * 8), pack_two<OT>(y[0][0], y[0][1]),
-                          pack_two<OT>(y[1][0], y[1][1]), pack_two<OT>(y[2][0], y[2][1]),
-                          pack_two<OT>(y[3][0], y[3][1]));
-      }
-    }
-  }
-
-  // The staged tokens (the first cnt) to Y from row m on, channels c .. c + n - 1.
-  __device__ static void write(const uint8_t* st, void* Y, int No, int64_t m, int cnt, int c, int n, int lane) {
-    constexpr int PER_ROW = CH / VEC, ROWS = 32 / PER_ROW;
-    uint8_t* y = static_cast<uint8_t*>(Y);
-    if (No % VEC == 0) {  // n is a multiple of VEC too
-      const int v = (lane % PER_ROW) * VEC;
-      if (v < n) {
 #pragma unroll
-        for (int t0 = 0; t0 < CHUNK; t0 += ROWS) {
-          const int t = t0 + lane / PER_ROW;
-          if (t < cnt)
-            *reinterpret_cast<uint4*>(y + ((m + t) * No + c + v) * SIZE) =
-                *reinterpret_cast<const uint4*>(st + at(t, v));
-        }
-      }
-    } else {
-      const int v = lane % CH;
-      for (int t = lane / CH; t < cnt; t += 32 / CH) {
-        if (v < n) {
-          if constexpr (k32)
-            reinterpret_cast<float*>(y)[(m + t) * No + c + v] = *reinterpret_cast<const float*>(st + at(t, v));
-          else
-            reinterpret_cast<uint16_t*>(y)[(m + t) * No + c + v] = *reinterpret_cast<const uint16_t*>(st + at(t, v));
+        for (int i = 0; i < 4; ++i) {
+          if (mine && (FULL || j0 + i < cnt)) store_out<OT>(y, 0, z[i]);
+          y += row_bytes;
         }
       }
     }
@@ -451,7 +380,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* sx_s = reinterpret_cast<float*>(smem + RING_BYTES + SLACK_BYTES);  // [2][MAX_BT]
+  float* sx_s = reinterpret_cast<float*>(smem + RING_BYTES);  // [2][MAX_BT]
   Groups groups;
   groups.off = reinterpret_cast<int*>(sx_s + 2 * MAX_BT);
   groups.cum = groups.off + MAX_GROUPS + 1;
@@ -667,30 +596,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int q = warp & 3;                   // TMEM lane quadrant of this warp
     const int set = (warp - 2) >> 2;          // sets of 4 warps take turns at the columns
     const int etid = static_cast<int>(threadIdx.x) - 64;
-    uint8_t* staging = smem + RING_BYTES + (warp - 2) * STAGING_BYTES;
     const int tile_ch = GATED ? p.H / 2 : p.H;  // channels of this CTA's tile
     // What a tile's outputs need from global memory, fetched while the tile
     // before it is written: a token's scale (one thread each) and this lane's
     // channel scales and biases.  (Fetched at its own turn, it made 3400 cycles
     // between two tiles.)
     struct Ahead {
-      int m0, tok, c, n;  // rows of Y; this warp's channels: n from c on inside Y and the tile
-      float sx, sw[4], b[4];
+      int m0, tok, c;  // rows of Y; this lane's channel
+      bool some, mine;  // the warp has channels inside Y and the tile; this lane's is one
+      float sx, sw, b;
     };
     auto fetch = [&](const Tile& t) {
       Ahead a;
       a.m0 = t.row;
       a.tok = t.tokens;
-      a.c = (2 * t.nt + rank) * tile_ch + q * Epi::CH;
-      a.n = min(min(tile_ch - q * Epi::CH, Epi::CH), p.No - a.c);
+      const int c0 = q * Epi::CH, ch = GATED ? lane & 15 : lane;
+      a.c = (2 * t.nt + rank) * tile_ch + c0 + ch;
+      a.some = c0 < tile_ch && a.c - ch < p.No;
+      a.mine = c0 + ch < tile_ch && a.c < p.No;
       a.sx = etid < a.tok ? p.sx[a.m0 + etid] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // TMEM lanes l / 4 + 8 i of the quadrant
-        const int ch = (lane >> 2) + 8 * (GATED ? i & 1 : i);
-        const int64_t at = static_cast<int64_t>(t.g) * p.N + a.c + ch + (GATED && i >= 2 ? p.No : 0);
-        a.sw[i] = ch < a.n ? p.sw[at] : 0.0f;
-        a.b[i] = ch < a.n && p.bias ? p.bias[at] : 0.0f;
-      }
+      const int64_t at = static_cast<int64_t>(t.g) * p.N + a.c + (GATED && lane >= 16 ? p.No : 0);
+      a.sw = a.mine ? p.sw[at] : 0.0f;
+      a.b = a.mine && p.bias ? p.bias[at] : 0.0f;
       return a;
     };
     static_assert(32 * EPI_WARPS >= MAX_BT, "a thread for each token's scale");
@@ -717,12 +644,21 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (more) next = fetch(t);
       const uint32_t addr =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * MAX_BT);
-      if (a.n > 0) {
+      if (a.some) {
+        constexpr int SIZE = OT == kF32 ? 4 : 2;
+        const int64_t row_bytes = static_cast<int64_t>(p.No) * SIZE;
         for (int c0 = set * Epi::CHUNK; c0 < a.tok; c0 += EPI_WARPS / 4 * Epi::CHUNK) {
-          Epi::stage(staging, addr + c0, lane, sxb + c0, a.sw, a.b);
-          __syncwarp();
-          Epi::write(staging, p.Y, p.No, a.m0 + c0, min(Epi::CHUNK, a.tok - c0), a.c, a.n, lane);
-          __syncwarp();
+          uint32_t r[Epi::CHUNK];
+          tmem_ld32(addr + c0, r);
+          tmem_ld_wait();
+          tmem_regs_ready(r);
+          uint8_t* y = static_cast<uint8_t*>(p.Y) + (a.m0 + c0 + (GATED && lane >= 16 ? 1 : 0)) * row_bytes +
+                       static_cast<int64_t>(a.c) * SIZE;
+          const int cnt = a.tok - c0;
+          if (cnt >= Epi::CHUNK)
+            Epi::template write<true>(r, sxb + c0, a.sw, a.b, a.mine, cnt, lane, y, row_bytes);
+          else
+            Epi::template write<false>(r, sxb + c0, a.sw, a.b, a.mine, cnt, lane, y, row_bytes);
         }
       }
       // This warp has read its columns: the MMAs of the tile after next may
