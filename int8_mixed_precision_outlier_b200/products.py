@@ -13,7 +13,8 @@ from __future__ import annotations
 
 import torch
 
-from .llmint8 import _check, _need, load_library
+from . import llmint8 as _base
+from .llmint8 import _check, _need
 
 _F16, _BF16, _F32 = torch.float16, torch.bfloat16, torch.float32
 _I8, _I32, _I64 = torch.int8, torch.int32, torch.int64
@@ -21,8 +22,14 @@ _DTYPES = {_F16: 0, _BF16: 1, _F32: 2}
 MAX_EXPERTS = 1024
 
 _Tensor = torch.Tensor
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the pointer alone: 3 us less than a Stream object
-_current_device = torch.cuda.current_device
+# The stream's pointer and the device's index alone: 3 us less than by way of a
+# Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _lib():
+    return _base._LIB or _base.load_library()
 
 
 def _refuse(t, dtype, shape, name, index):
@@ -133,7 +140,7 @@ def _launch_quantize(X, positions, Xq, xscale, S, st):
     if xscale is None:
         xscale = torch.empty(S, dtype=_F32, device=X.device)
     at, copies = (None, 0) if positions is None else (positions.data_ptr(), positions.shape[1])
-    rc = load_library().llmint8_quantize_rows(X.data_ptr(), _DTYPES[X.dtype], T, K, at, copies, S, Xq.data_ptr(),
+    rc = _lib().llmint8_quantize_rows(X.data_ptr(), _DTYPES[X.dtype], T, K, at, copies, S, Xq.data_ptr(),
                                               xscale.data_ptr(), st)
     if rc:
         _check(rc, "llmint8_quantize_rows")
@@ -198,7 +205,7 @@ def _launch_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, st, 
     if Y is None:
         Y = torch.empty(S, N // 2 if gated else N, dtype=dtype, device=Xq.device)
     b = None if bias is None else bias.data_ptr()
-    lib = load_library()
+    lib = _lib()
     if offsets is None:
         rc = lib.llmint8_scaled_matmul(Xq.data_ptr(), xscale.data_ptr(), S, K, Wq.data_ptr(), Wscale.data_ptr(), b, N,
                                        1 if gated else 0, Y.data_ptr(), _DTYPES[dtype], st)
@@ -275,7 +282,7 @@ def _launch_positions(ids, experts, positions, offsets, st):
         positions = torch.empty(T, k, dtype=_I32, device=ids.device)
     if offsets is None:
         offsets = torch.empty(experts + 1, dtype=_I32, device=ids.device)
-    rc = load_library().llmint8_expert_positions(ids.data_ptr(), 8 if ids.dtype is _I64 else 4, T, k, experts,
+    rc = _lib().llmint8_expert_positions(ids.data_ptr(), 8 if ids.dtype is _I64 else 4, T, k, experts,
                                                  positions.data_ptr(), offsets.data_ptr(), st)
     if rc:
         _check(rc, "llmint8_expert_positions")
@@ -325,7 +332,7 @@ def _launch_combine(Y, positions, weights, dtype, out, st):
     T, k = positions.shape
     if out is None:
         out = torch.empty(T, N, dtype=dtype, device=Y.device)
-    rc = load_library().llmint8_expert_combine(Y.data_ptr(), _DTYPES[Y.dtype], S, N, positions.data_ptr(),
+    rc = _lib().llmint8_expert_combine(Y.data_ptr(), _DTYPES[Y.dtype], S, N, positions.data_ptr(),
                                                weights.data_ptr(), T, k, out.data_ptr(), _DTYPES[dtype], st)
     if rc:
         _check(rc, "llmint8_expert_combine")

@@ -522,6 +522,55 @@ def test_weights_quantised_by_the_call_before(L):
     assert all(torch.equal(x, y) for x, y in got)
 
 
+def test_two_captured_graphs_at_once(L):
+    """Two graphs with the same layer in each, replayed on two streams at the same time."""
+    g = gen(31)
+    T, k, E, K, F = 120, 2, 4, 512, 256
+    W1 = (codes(g, E, 2 * F, K), scales(g, 0.02 / K ** 0.5, E, 2 * F))
+    W2 = (codes(g, E, K, F), scales(g, 0.02 / F ** 0.5, E, K))
+    runs = []
+    for _ in range(2):
+        X = torch.randn(T, K, generator=g, device="cuda").half()
+        ids = torch.randint(0, E, (T, k), generator=g, device="cuda")
+        w = torch.rand(T, k, generator=g, device="cuda")
+        want, _ = mixture(L, X, ids, w, W1, W2)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out, kept = mixture(L, X, ids, w, W1, W2)
+        runs.append((graph, torch.cuda.Stream(), out, want, kept, X, ids, w))
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, out, want, *_ in runs:
+        assert torch.equal(out, want)
+
+
+def test_offsets_past_32_bits(L):
+    """Outputs, codes and inputs of more than 2^31 elements: the first and the last rows."""
+    g = gen(1)
+    T, N, K = 140000, 16384, 16
+    ends = [0, 1, T // 2, T - 2, T - 1]
+    Xq, Wq = codes(g, T, K), codes(g, N, K)
+    sx, sw = scales(g, 0.02, T), scales(g, 0.02, N)
+    Y = L.llmint8_scaled_matmul(Xq, sx, Wq, sw, dtype=torch.bfloat16)
+    check(Y[ends], *expected(Xq[ends], sx[ends], Wq, sw, None, False, torch.bfloat16))
+    q, s = L.llmint8_quantize_rows(Y)
+    q0, s0 = quantized(Y[ends])
+    assert torch.equal(q[ends], q0) and torch.equal(s[ends], s0)
+    positions = torch.tensor([[T - 1, 0], [T - 2, T - 1]], dtype=torch.int32, device="cuda")
+    out = L.llmint8_expert_combine(Y, positions, torch.ones(2, 2, device="cuda"), dtype=torch.float32)
+    rows_ = Y[positions.long()].float()
+    assert torch.equal(out, rows_[:, 0] + rows_[:, 1])
+    q.zero_()
+    at = torch.full((3, 1), T - 1, dtype=torch.int32, device="cuda") - torch.arange(3, dtype=torch.int32, device="cuda")[:, None]
+    L.llmint8_quantize_rows(Y[:3].contiguous(), at, q, s)
+    assert torch.equal(q[[T - 1, T - 2, T - 3]], quantized(Y[:3])[0]) and not q[: T - 3].any()
+
+
 def test_refusals(L):
     g = gen(0)
     Xq, Wq = codes(g, 8, 64), codes(g, 32, 64)
