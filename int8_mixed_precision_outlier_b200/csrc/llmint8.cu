@@ -657,8 +657,10 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   ProductPlan best;
   // A CTA pair runs its tiles one after the other, `rounds` in all; a tile
   // costs KB steps.  A step was measured at 0.04 us + 1.04 ns a token column
-  // (the MMA's own time: its rate does not fall with fewer weight rows) + 0.4
-  // ns a weight row of the CTA (the copies; below 64 rows they cost no less):
+  // (the MMA's own time, which does not fall with fewer weight rows, nor below
+  // 64 columns) + 0.4 ns a weight row of the CTA (the copies; below 64 rows they
+  // cost no less), the last tile's outputs at 6 ns a column, and a wave
+  // that is cut finer reads more operands (0.7 us for a full one):
   // 333 x 13824 x 5120 takes 24.4 us with 2 rounds of 176 x 192, 29.3 with 176
   // x 256, 27.5 with 3 rounds of 96 x 256.
   double best_cost = -1.0;
@@ -667,8 +669,10 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
     // many tiles of different lengths even out
     const double rounds = grouped && tiles > 4.0 ? tiles : std::ceil(tiles);
     const int cols = up16((avg + mt - 1) / mt);
-    const double cost = rounds * (KB * (0.04 + 0.00104 * cols + 0.0004 * std::max(H, 64)) + 0.5);
-    if (best_cost < 0.0 || cost <= best_cost) {
+    const double cost =
+        rounds * (KB * (0.04 + 0.00104 * std::max(cols, 64) + 0.0004 * std::max(H, 64)) + 0.5) + 0.006 * cols +
+        0.7 * std::min(tiles, 1.0);
+    if (best_cost < 0.0 || cost < best_cost) {
       best_cost = cost;
       best.H = H;
       best.BT = BT;

@@ -37,7 +37,7 @@ constexpr int BK = 128;            // bytes of K per k-block
 constexpr int MAX_BT = 256;        // most tokens of a tile (MMA N)
 constexpr int KPB_MAX = 4;         // k-blocks per stage
 constexpr int MAX_STAGES = 12;
-constexpr int MAX_GROUPS = 1024;
+constexpr int MAX_GROUPS = 1024;   // 32 * 32: see Walk::search
 constexpr int EPI_WARPS = 16;
 constexpr int PLAN_WARP = 2 + EPI_WARPS;
 constexpr int THREADS = 32 * (PLAN_WARP + 1);
@@ -133,7 +133,7 @@ __device__ __forceinline__ int small_div(int a, int b) {
   return __float2int_rz(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b)));
 }
 
-// The tiles w = unit, unit + units, ... of a CTA (pair).  Within a group the
+// The tiles w = unit, unit + units, ... of a CTA pair, walked by one warp.  Within a group the
 // token tiles of one weight tile come one after the other (the weights are
 // then read from L2); moving on needs no division of large numbers: only the
 // step `units` and the rest below it are divided.
@@ -156,23 +156,19 @@ struct Walk {
     dq = small_div(units, mt);
     dr = units - dq * mt;
   }
-  // The group whose tiles hold w, from group `lo` on.
-  __device__ void search(const Params& p, const Groups& s, int lo) {
-    int hi = p.E;  // cum[lo] <= w < cum[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s.cum[mid] <= w)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    enter(s, lo);
+  // The group whose tiles hold w (cum[g] <= w < cum[g + 1]), by the whole warp:
+  // first the 32 groups it is among, then the group, 32 counts at a time.
+  __device__ void search(const Params& p, const Groups& s) {
+    const int lane = static_cast<int>(lane_id());
+    const int block = __popc(__ballot_sync(0xffffffffu, (lane + 1) * 32 < p.E && s.cum[min((lane + 1) * 32, p.E)] <= w));
+    const int g0 = block * 32 + lane + 1;
+    enter(s, block * 32 + __popc(__ballot_sync(0xffffffffu, g0 < p.E && s.cum[min(g0, p.E)] <= w)));
   }
   __device__ Walk(const Params& p, const Groups& s, int unit, int step) {
     w = unit;
     units = step;
     total = s.cum[p.E];
-    if (w < total) search(p, s, 0);
+    if (w < total) search(p, s);
   }
   __device__ bool more() const { return w < total; }
   __device__ void next(const Params& p, const Groups& s) {
@@ -186,7 +182,7 @@ struct Walk {
         ++nt;
       }
     } else if (w < total) {
-      search(p, s, g + 1);
+      search(p, s);
     }
   }
   __device__ int row() const { return begin + i * per; }                  // first row of Xq / Y

@@ -154,10 +154,10 @@ def test_tile_arithmetic(BT):
 
 
 def find_tile(off, cum, BT, w):
-    lo, hi = 0, len(cum) - 1
-    while hi - lo > 1:
-        mid = (lo + hi) // 2
-        lo, hi = (mid, hi) if cum[mid] <= w else (lo, mid)
+    E = len(cum) - 1
+    block = sum((i + 1) * 32 < E and cum[min((i + 1) * 32, E)] <= w for i in range(32))
+    lo = block * 32 + sum(block * 32 + i + 1 < E and cum[min(block * 32 + i + 1, E)] <= w for i in range(32))
+    assert cum[lo] <= w < cum[lo + 1]
     begin, m = off[lo], off[lo + 1] - off[lo]
     mt = -(-m // BT)
     assert mt == token_tiles(m, BT)
@@ -171,7 +171,7 @@ def find_tile(off, cum, BT, w):
 def test_tiles_cover_every_row_once(BT):
     rng = np.random.default_rng(BT)
     for trial in range(40):
-        E = int(rng.integers(1, 70))
+        E = int(rng.choice([1, 2, 31, 32, 33, 64, 65, 70, 1024])) if trial % 4 == 0 else int(rng.integers(1, 70))
         sizes = rng.integers(0, rng.choice([2, 18, 300, 1100]), E) * (rng.random(E) < 0.7)
         lead, tail = int(rng.integers(0, 3)), int(rng.integers(0, 5))
         offsets = (lead + np.concatenate([[0], np.cumsum(sizes)])).tolist()
