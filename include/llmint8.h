@@ -325,7 +325,7 @@ LLMINT8_API int llmint8_smoothquant_matmul_debug(const void* X, int64_t T, int64
  * these entries take codes that are already there (one quantised input serves
  * several projections, or several experts) and serve inference only.
  * None takes a workspace, so calls on several streams, or in several captured
- * graphs, do not meet.  K <= 65536.
+ * graphs, do not meet.  K <= 65536; a product has at most 2^31 - 257 rows and 2^31 - 257 weight rows.
  */
 typedef enum { LLMINT8_F16 = 0, LLMINT8_BF16 = 1, LLMINT8_F32 = 2 } llmint8_dtype;
 

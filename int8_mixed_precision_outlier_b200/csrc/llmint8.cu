@@ -650,10 +650,10 @@ struct ProductPlan {
 
 ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, int max_pairs) {
   const int groups = grouped ? std::min(E, S) : 1;
-  const int avg = (S + groups - 1) / groups;  // tokens of a group
+  const int64_t avg = (static_cast<int64_t>(S) + groups - 1) / groups;  // tokens of a group
   const bool ksplit = K % product::BK == 0;
   const int KB = (K + product::BK - 1) / product::BK;
-  auto up16 = [](int x) { return (x + 15) / 16 * 16; };
+  auto up16 = [](int64_t x) { return static_cast<int>((x + 15) / 16 * 16); };
   ProductPlan best;
   // A CTA pair runs its tiles one after the other, `rounds` in all; a tile
   // costs KB steps.  A step was measured at 0.04 us + 1.04 ns a token column
@@ -664,8 +664,8 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   // 333 x 13824 x 5120 takes 24.4 us with 2 rounds of 176 x 192, 29.3 with 176
   // x 256, 27.5 with 3 rounds of 96 x 256.
   double best_cost = -1.0;
-  auto consider = [&](int H, int nN, int BT, int mt) {
-    const double tiles = static_cast<double>(groups) * mt * nN / max_pairs;
+  auto consider = [&](int H, int nN, int BT, int64_t mt) {
+    const double tiles = static_cast<double>(groups) * static_cast<double>(mt) * nN / max_pairs;
     // many tiles of different lengths even out
     const double rounds = grouped && tiles > 4.0 ? tiles : std::ceil(tiles);
     const int cols = up16((avg + mt - 1) / mt);
@@ -681,14 +681,14 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   };
   const int step = gated ? 32 : 8;
   for (int H = step; H <= product::BM; H += step) {
-    const int nN = (N + 2 * H - 1) / (2 * H);
+    const int nN = static_cast<int>((static_cast<int64_t>(N) + 2 * H - 1) / (2 * H));
     if (grouped) {
       // room for groups twice as long as the average without a second tile
-      const int BT = std::min(product::MAX_BT, up16(std::min(2 * avg, product::MAX_BT) + 16));
+      const int BT = std::min(product::MAX_BT, up16(std::min<int64_t>(2 * avg, product::MAX_BT) + 16));
       consider(H, nN, BT, (avg + BT - 1) / BT);
     } else {
-      const int least = (avg + product::MAX_BT - 1) / product::MAX_BT;
-      for (int mt = least; mt <= least + 8 && (mt == least || avg > 32 * (mt - 1)); ++mt)
+      const int64_t least = (avg + product::MAX_BT - 1) / product::MAX_BT;
+      for (int64_t mt = least; mt <= least + 8 && (mt == least || avg > 32 * (mt - 1)); ++mt)
         consider(H, nN, up16((avg + mt - 1) / mt), mt);
     }
   }
@@ -721,7 +721,7 @@ ProductKernel product_kernel_for(int dtype) {
 int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const int32_t* offsets, bool grouped,
                  int64_t E, const int8_t* Wq, const float* sw, const float* bias, int64_t N, int gated, void* Y,
                  int dtype, void* stream) {
-  if (S < 0 || N < 0 || S > INT32_MAX - product::MAX_BT || N > INT32_MAX || K < 16 || K > kMaxK)
+  if (S < 0 || N < 0 || S > INT32_MAX - product::MAX_BT || N > INT32_MAX - 2 * product::BM || K < 16 || K > kMaxK)
     return LLMINT8_ERR_INVALID_ARG;
   if (E < 1 || E > product::MAX_GROUPS || !float_dtype(dtype)) return LLMINT8_ERR_INVALID_ARG;
   if (gated && N % 32 != 0) return LLMINT8_ERR_INVALID_ARG;

@@ -571,6 +571,25 @@ def test_offsets_past_32_bits(L):
     assert torch.equal(q[[T - 1, T - 2, T - 3]], quantized(Y[:3])[0]) and not q[: T - 3].any()
 
 
+def test_more_than_2_30_rows(L):
+    """One group of more than 2^30 rows, of which 160 at its start and its end hold something: twice its length and its
+    rounded-up parts pass 32 bits."""
+    g = gen(2)
+    S, N, K = (1 << 30) + 4097, 16, 16
+    some = torch.cat([torch.arange(80), torch.arange(S - 80, S)]).cuda()
+    Xq = torch.zeros(S, K, dtype=torch.int8, device="cuda")
+    Xq[some] = codes(g, 160, K)
+    sx = torch.full((S,), 0.5, device="cuda")
+    Wq, sw = codes(g, 1, N, K), scales(g, 0.02, 1, N)
+    want, tol = expected(Xq[some], sx[some], Wq[0], sw[0], None, False, torch.float16)
+    offsets = torch.tensor([0, S], dtype=torch.int32, device="cuda")
+    Y = L.llmint8_grouped_matmul(Xq, sx, offsets, Wq, sw)
+    check(Y[some], want, tol, "grouped")
+    assert not Y[80:S - 80].any()
+    Y = None
+    check(L.llmint8_scaled_matmul(Xq, sx, Wq[0], sw[0])[some], want, tol, "dense")
+
+
 def test_refusals(L):
     g = gen(0)
     Xq, Wq = codes(g, 8, 64), codes(g, 32, 64)

@@ -44,6 +44,13 @@ def test_scaled_matmul_refusals(lib):
     assert scaled(lib, T=0, Xq=None, sx=None, Y=None) == OK and scaled(lib, N=0, Wq=None, sw=None, Y=None) == OK
 
 
+def test_products_refuse_sizes_whose_tiles_pass_32_bits(lib):
+    """The last tile of the channels ends up to 255 rows past N, the last tile of the tokens 255 past S."""
+    last = (1 << 31) - 1
+    assert scaled(lib, N=last - 255, K=16) == INVALID and scaled(lib, T=last - 255, K=16) == INVALID
+    assert grouped(lib, N=last - 255, K=16) == INVALID and grouped(lib, S=last - 255, K=16) == INVALID
+
+
 def test_grouped_matmul_refusals(lib):
     assert grouped(lib, E=0) == INVALID and grouped(lib, E=1025) == INVALID
     assert grouped(lib, offsets=None) == INVALID and grouped(lib, offsets=ODD) == ALIGNMENT
