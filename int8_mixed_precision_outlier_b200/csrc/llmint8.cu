@@ -73,6 +73,18 @@ cudaError_t set_attributes() {
   return e;
 }
 
+using ProductKernel = void (*)(const CUtensorMap, const product::TokenMaps, const product::Params);
+template <bool GATED, bool WIDE>
+ProductKernel product_kernel_of(int dtype) {
+  return dtype == LLMINT8_F16    ? product::product_kernel<GATED, product::kF16, WIDE>
+         : dtype == LLMINT8_BF16 ? product::product_kernel<GATED, product::kBF16, WIDE>
+                                 : product::product_kernel<GATED, product::kF32, WIDE>;
+}
+template <bool GATED>
+ProductKernel product_kernel_for(int dtype, bool wide) {
+  return wide ? product_kernel_of<GATED, true>(dtype) : product_kernel_of<GATED, false>(dtype);
+}
+
 // Shared-memory limits of the products with token and channel scales and of
 // the expert positions.
 cudaError_t set_product_attributes() {
@@ -80,12 +92,11 @@ cudaError_t set_product_attributes() {
   auto big = [&](auto kern, int bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  big(product::product_kernel<false, product::kF16>, product::SMEM_BYTES);
-  big(product::product_kernel<false, product::kBF16>, product::SMEM_BYTES);
-  big(product::product_kernel<false, product::kF32>, product::SMEM_BYTES);
-  big(product::product_kernel<true, product::kF16>, product::SMEM_BYTES);
-  big(product::product_kernel<true, product::kBF16>, product::SMEM_BYTES);
-  big(product::product_kernel<true, product::kF32>, product::SMEM_BYTES);
+  for (const int dtype : {product::kF16, product::kBF16, product::kF32})
+    for (const bool wide : {false, true}) {
+      big(product_kernel_for<false>(dtype, wide), product::SMEM_BYTES);
+      big(product_kernel_for<true>(dtype, wide), product::SMEM_BYTES);
+    }
   auto positions = [&](auto kern) {
     big(kern, expert::pos_smem_bytes(product::MAX_GROUPS));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -645,6 +656,7 @@ bool float_dtype(int d) { return d == LLMINT8_F16 || d == LLMINT8_BF16 || d == L
 // lengths the device's offsets give.
 struct ProductPlan {
   int BT = 0, quarter = 0, b_rows = 0, KPB = 0, H = 0, stages = 0, nN = 0;
+  bool wide = false;  // tiles of two halves of BT tokens
   int64_t tiles = 0;  // an upper bound
 };
 
@@ -693,6 +705,28 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
     }
   }
   best.tiles = (static_cast<int64_t>(S) / best.BT + groups) * best.nN;
+  // Tiles of two halves of up to 256 tokens each, which share the copies of the
+  // weights and take both accumulators.  Nothing overlaps their outputs, so
+  // they pay where they save a round or narrow tiles: 333 x 13824 x 5120 takes
+  // 24.1 us with them and 25.6 without (27.8 and 30.7 at the sustained clock),
+  // 257 x 13824 x 5120 20.4 and 23.1, 1024 x 8192 x 8192 48.5 and 53.4; where
+  // the estimate says no, 512 x 27648 x 5120 61.9 and 52.8, 4096 x 28672 x 8192
+  // 685 and 651.
+  if (!grouped && avg > product::MAX_BT) {
+    const int H = product::BM, nN = static_cast<int>((static_cast<int64_t>(N) + 2 * H - 1) / (2 * H));
+    const int64_t wide = (avg + 2 * product::MAX_BT - 1) / (2 * product::MAX_BT);
+    const int half = up16((avg + 2 * wide - 1) / (2 * wide));
+    const double rounds = std::ceil(static_cast<double>(wide) * nN / max_pairs);
+    const double cost = rounds * (KB * (0.04 + 0.00104 * 2 * half + 0.0004 * H) + 0.5 + 0.006 * 2 * half) +
+                        0.7 * std::min(static_cast<double>(wide) * nN / max_pairs, 1.0);
+    if (cost < 0.95 * best_cost && (2 * wide - 1) * half < avg) {  // every half has rows
+      best.wide = true;
+      best.H = H;
+      best.BT = half;
+      best.nN = nN;
+      best.tiles = wide * nN;
+    }
+  }
   const int mine = best.BT / 2;  // token rows of a CTA
   best.quarter = (mine + 31) / 32 * 8;
   best.b_rows = (mine + best.quarter - 1) / best.quarter * best.quarter;
@@ -700,22 +734,14 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   // its products 2 a token column and k-block (160 at least), so stages of
   // narrow tiles hold more; four stages at least, or the loads wait.
   // 16 x 4096 x 4096: 11.1, 8.2, 7.3 us with 1, 2, 4 k-blocks.
-  const int cols = std::min(best.BT, up16(avg));
+  const int cols = std::min(best.BT << best.wide, up16(avg));
   const int wish = cols >= 224 ? 1 : cols >= 96 ? 2 : product::KPB_MAX;
-  const int kblock = (best.H + best.b_rows) * product::BK;
+  const int kblock = (best.H + (best.b_rows << best.wide)) * product::BK;
   best.KPB = 1;
   while (ksplit && best.KPB < wish && 2 * best.KPB <= KB && 4 * 2 * best.KPB * kblock <= product::RING_BYTES)
     best.KPB *= 2;
   best.stages = std::min(product::MAX_STAGES, product::RING_BYTES / (kblock * best.KPB));
   return best;
-}
-
-using ProductKernel = void (*)(const CUtensorMap, const product::TokenMaps, const product::Params);
-template <bool GATED>
-ProductKernel product_kernel_for(int dtype) {
-  return dtype == LLMINT8_F16    ? product::product_kernel<GATED, product::kF16>
-         : dtype == LLMINT8_BF16 ? product::product_kernel<GATED, product::kBF16>
-                                 : product::product_kernel<GATED, product::kF32>;
 }
 
 int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const int32_t* offsets, bool grouped,
@@ -754,6 +780,7 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   p.count = product::tile_count(plan.BT);
   p.mt = grouped ? 0 : product::token_tiles(p.S, p.count);
   p.per = product::tile_rows(p.S, p.mt, plan.BT);
+  p.mt >>= plan.wide;
   p.quarter = plan.quarter;
   p.b_rows = plan.b_rows;
   p.stages = plan.stages;
@@ -782,7 +809,7 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   for (int i = 0; i < 4; ++i)
     if (i < least || i * p.quarter >= p.b_rows) tx.m[i] = tx.m[least];
   if (!ok) return LLMINT8_ERR_CUDA;
-  const ProductKernel kern = gated ? product_kernel_for<true>(dtype) : product_kernel_for<false>(dtype);
+  const ProductKernel kern = gated ? product_kernel_for<true>(dtype, plan.wide) : product_kernel_for<false>(dtype, plan.wide);
   const int pairs = static_cast<int>(std::min<int64_t>(max_pairs, plan.tiles));
   const cudaError_t e = launch_ex(kern, dim3(2 * pairs), dim3(product::THREADS), product::SMEM_BYTES,
                                   static_cast<cudaStream_t>(stream), true, 2, tw, tx, p);

@@ -88,7 +88,7 @@ struct Params {
   int H;               // weight rows of a tile and CTA (a multiple of 8; of 32 when gated)
   int nN;              // tiles along the channels (2 H rows each for CTA pairs)
   int BT;              // most tokens of a tile, a multiple of 16
-  int mt, per;         // without offsets: token tiles, rows of each
+  int mt, per;         // without offsets: token tiles, rows of each (of each half, where they have two)
   TileCount count;     // of BT
   int quarter;         // token rows of a copy come in 1..4 quarters (a multiple of 8 rows each)
   int b_rows;          // token rows that a k-block of a stage has room for
@@ -185,8 +185,11 @@ struct Walk {
       search(p, s);
     }
   }
-  __device__ int row() const { return begin + i * per; }                  // first row of Xq / Y
-  __device__ int tokens() const { return min(per, rows - i * per); }
+  // Group, tile along the channels, first row of Xq / Y, rows; `half` 0 or 1 of a tile of two.
+  __device__ int4 tile(bool wide, int half) const {
+    const int at = ((i << wide) + half) * per;
+    return make_int4(g, nt, begin + at, min(per, rows - at));
+  }
 };
 
 // Fills the groups' tables, by one warp.  Bounds that fall outside [0, S] or
@@ -369,7 +372,12 @@ __device__ __forceinline__ int quarters_of(const Params& p, int rows) {
 // `full` barriers, and each commit arrives at both CTAs.  (Single CTAs with
 // tiles of 128 rows were within 3 % of pairs on the smallest shapes, up to
 // 27 % behind on others.)
-template <bool GATED, int OT>
+//
+// WIDE tiles have two halves of up to MAX_BT tokens, one accumulator
+// each: a stage brings the weights once and the token rows of both, and the
+// products of both follow.  For the planner and the epilogue the halves are
+// two tiles, one after the other.
+template <bool GATED, int OT, bool WIDE>
 __global__ void __launch_bounds__(THREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ TokenMaps tmaps_x,
                    const Params p) {
@@ -436,9 +444,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int a_bytes = p.H * BK;                     // of one k-block
   const int b_bytes = p.b_rows * BK;
-  const int stage_bytes = (a_bytes + b_bytes) * p.KPB;
+  const int half_bytes = b_bytes * p.KPB;           // the token rows of a stage (of one half)
+  const int stage_bytes = a_bytes * p.KPB + (half_bytes << WIDE);
   auto stage_b = [&](int s) { return smem + s * stage_bytes; };
-  auto stage_a = [&](int s) { return smem + s * stage_bytes + p.KPB * b_bytes; };
+  auto stage_a = [&](int s) { return smem + s * stage_bytes + (half_bytes << WIDE); };
 
   // A wait of a whole warp with one outcome: lanes that gave up and lanes that
   // did not would part, and never meet again at a warp-wide step.  (The loops
@@ -474,18 +483,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
     Walk t(p, groups, unit, units);
     bool ok = true;
-    for (int i = 0; ok; ++i) {
+    for (int i = 0, half = 0; ok; ++i) {
       const int slot = i % AHEAD;
       ok = i < AHEAD || all_wait(&taken[slot], ((i / AHEAD) & 1) ^ 1, kErrTimeoutProducer);
       const bool more = ok && t.more();
       if (lane == 0) {
-        tiles[slot] = more ? make_int4(t.g, t.nt, t.row(), t.tokens()) : make_int4(-1, 0, 0, 0);
+        tiles[slot] = more ? t.tile(WIDE, half) : make_int4(-1, 0, 0, 0);
         mbar_arrive(&planned[slot]);
       }
       __syncwarp();
       if (!more) break;
       if (i == 0 && !ragged) previous_done();  // without offsets nothing here waits for it
-      t.next(p, groups);
+      if (half == WIDE) t.next(p, groups);
+      half ^= WIDE;
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -498,13 +508,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t phase = 1;     // parity its `empty` barrier had before this round (passes at once in round 0)
     bool ok = true;
     int i = 0;
-    for (Tile t; ok && take(i, t);) {
+    for (Tile t, t2; ok && take(i, t);) {
+      if (WIDE && !take(i, t2)) break;
       const int mine = (t.tokens + 15) / 16 * 8;  // token rows this CTA copies: half the MMA's N
       const int wt = 2 * t.nt + rank;             // this CTA's weight rows, in units of H
       const int x0 = t.row + rank * mine;
       const int quarters = quarters_of(p, mine);
       const CUtensorMap* tmap_x = &tmaps_x.m[quarters - 1];
-      const uint32_t tx = static_cast<uint32_t>(2 * p.KPB * (a_bytes + quarters * p.quarter * BK));
+      const int mine2 = WIDE ? (t2.tokens + 15) / 16 * 8 : 0, x2 = WIDE ? t2.row + rank * mine2 : 0;
+      const int quarters2 = WIDE ? quarters_of(p, mine2) : 0;
+      const uint32_t tx = static_cast<uint32_t>(2 * p.KPB * (a_bytes + (quarters + quarters2) * p.quarter * BK));
       for (int u = 0; u < p.NU; ++u) {
         ok = mbar_wait_stage(&empty[s], phase, p.wait_ns, kErrTimeoutProducer);
         if (!ok) break;
@@ -517,6 +530,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           else
             tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.g);
           tma_load_3d_pair(stage_b(s), tmap_x, bar, x, x0, kb);
+          if constexpr (WIDE) tma_load_3d_pair(stage_b(s) + half_bytes, &tmaps_x.m[quarters2 - 1], bar, x, x2, kb);
         }
         if (++s == p.stages) {
           s = 0;
@@ -533,21 +547,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     previous_done();
     if (rank == 0) {
       const uint32_t ring = sdesc_low(smem_addr(smem)), stage_step = static_cast<uint32_t>(stage_bytes) >> 4;
-      const uint32_t a_at = static_cast<uint32_t>(p.KPB * b_bytes) >> 4, a_step = static_cast<uint32_t>(a_bytes) >> 4;
+      const uint32_t half_at = static_cast<uint32_t>(half_bytes) >> 4;
+      const uint32_t a_at = half_at << WIDE, a_step = static_cast<uint32_t>(a_bytes) >> 4;
       int s = 0, tc = 0;
       uint32_t phase = 0, stage = ring;  // `stage`: descriptor of the stage's token rows
       bool ok = true, ready = false;
       int i = 0;
-      for (Tile t; ok && take(i, t); ++tc) {
+      for (Tile t, t2; ok && take(i, t); tc += 1 + WIDE) {
+        if (WIDE && !take(i, t2)) break;
         const int cols = (t.tokens + 15) / 16 * 16;
         const uint32_t idesc = idesc_i8_s32(2 * BM, cols);
         // k-blocks of a stage lie as the copy put them: its rows apart
         const uint32_t b_step = static_cast<uint32_t>(quarters_of(p, cols / 2) * p.quarter * BK) >> 4;
-        uint32_t add = 0;  // the tile's first product overwrites the accumulator
+        const int cols2 = WIDE ? (t2.tokens + 15) / 16 * 16 : 0;
+        const uint32_t idesc2 = idesc_i8_s32(2 * BM, WIDE ? cols2 : 16);
+        const uint32_t b_step2 = static_cast<uint32_t>(quarters_of(p, cols2 / 2) * p.quarter * BK) >> 4;
         const int buf = tc & 1;
         if (tc >= 2) {
           ok = __all_sync(0xffffffffu,
                           mbar_wait_stage<true>(&tempty[buf], ((tc >> 1) - 1) & 1, p.wait_ns, kErrTimeoutMma));
+          if constexpr (WIDE)
+            ok = __all_sync(0xffffffffu,
+                            ok && mbar_wait_stage<true>(&tempty[1], ((tc >> 1) - 1) & 1, p.wait_ns, kErrTimeoutMma));
           if (!ok) break;
         }
         tc_fence_after();
@@ -568,19 +589,26 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_fence_after();
           if (issuer) {
             const int nkb = u + 1 < p.NU ? p.KPB : p.KB - u * p.KPB;
-            uint32_t blow = here, alow = here + a_at;
-            for (int j = 0; j < nkb; ++j, alow += a_step, blow += b_step) {
+            auto products = [&](uint32_t acc, uint32_t blow, uint32_t step, uint32_t id) {
+              uint32_t alow = here + a_at, add = u > 0;  // the tile's first product overwrites the accumulator
+              for (int j = 0; j < nkb; ++j, alow += a_step, blow += step) {
 #pragma unroll
-              for (int k = 0; k < BK / 32; ++k) {
-                mma_i8_low_pair(d, alow + 2 * k, blow + 2 * k, idesc, add);
-                add = 1;
+                for (int k = 0; k < BK / 32; ++k) {
+                  mma_i8_low_pair(acc, alow + 2 * k, blow + 2 * k, id, add);
+                  add = 1;
+                }
               }
-            }
+            };
+            products(d, here, b_step, idesc);
+            if constexpr (WIDE) products(d + MAX_BT, here + half_at, b_step2, idesc2);
             mma_commit_pair(freed, 0x3);
           }
         }
         ok = __all_sync(0xffffffffu, ok);
-        if (ok && issuer) mma_commit_pair(&tfull[buf], 0x3);
+        if (ok && issuer) {
+          mma_commit_pair(&tfull[buf], 0x3);
+          if constexpr (WIDE) mma_commit_pair(&tfull[1], 0x3);
+        }
       }
       if (issuer) mma_commit_pair(done, 0x3);
     }

@@ -121,6 +121,25 @@ def test_scaled_matmul_gated(L, T, F, K, dtype):
         untouched()
 
 
+FEW_TILES = [(333, 13824, 144, False), (257, 9999, 256, False), (150, 40000, 128, False), (16, 40008, 1040, False),
+              (500, 19968, 272, True), (1111, 8000, 640, False), (47, 64000, 512, True),
+              (257, 13824, 2048, False), (270, 18944, 2064, True), (600, 9001, 4096, False), (513, 8192, 4112, True)]
+
+
+@pytest.mark.parametrize("T,N,K,gated", FEW_TILES)
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_scaled_matmul_of_a_few_tiles_per_sm(L, T, N, K, gated, dtype):
+    """One to four tiles for each pair of SMs; tiles of two halves, full and ragged, with and without a K tail."""
+    g = gen(T + N)
+    Xq, Wq = codes(g, T, K), codes(g, N, K)
+    sx, sw = scales(g, 0.01, T), scales(g, 0.001, N)
+    b = torch.randn(N, generator=g, device="cuda")
+    Y, untouched = fenced(T, N // 2 if gated else N, dtype)
+    L.llmint8_scaled_matmul(Xq, sx, Wq, sw, b, gated=gated, Y=Y)
+    check(Y, *expected(Xq, sx, Wq, sw, b, gated, dtype))
+    untouched()
+
+
 def test_scaled_matmul_is_exact_on_integers(L):
     """Unit scales, float32 output: the int32 sums themselves, at codes of the largest magnitudes and the largest K
     (sums up to 2^30 round to binary32 once)."""

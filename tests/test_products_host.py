@@ -194,6 +194,22 @@ def test_tiles_cover_every_row_once(BT):
         assert not seen[:offsets[0]].any() and not seen[offsets[-1]:].any()
 
 
+def test_tiles_of_two_halves_cover_every_row_once():
+    """Where every half has rows (the others are not cut this way); the kernel finds the tile i // 2 and its halves."""
+    cut = 0
+    for S in list(range(257, 3000)) + [2 ** 31 - 257, 2 ** 30 + 1]:
+        wide = (S + 511) // 512
+        half = -(-S // (2 * wide)) + 15 & ~15
+        assert half <= 256
+        if (2 * wide - 1) * half >= S:
+            continue
+        cut += 1
+        mt = token_tiles(S, half)
+        per = tile_rows(S, mt, half)
+        assert mt == 2 * wide and per <= half and per * mt >= S and per * (mt - 1) < S
+    assert cut > 2000
+
+
 @pytest.mark.parametrize("offsets", [[0, 5, 3, 9], [-4, 2, 2, 2], [0, 1 << 30, 4, 10], [7, 7, 2, 99], [3, 1, 0, -1]])
 def test_wrong_bounds_stay_inside(offsets):
     S = 10
