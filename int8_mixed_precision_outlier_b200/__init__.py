@@ -14,6 +14,6 @@ from .llmint8 import (  # noqa: F401
     llmint8_matmul_stored,
 )
 from .products import (  # noqa: F401
-    MAX_EXPERTS, Int8Experts, llmint8_expert_combine, llmint8_expert_positions, llmint8_grouped_matmul, llmint8_quantize_rows,
-    llmint8_scaled_matmul,
+    MAX_EXPERTS, Int8Experts, llmint8_expert_combine, llmint8_expert_positions, llmint8_grouped_matmul,
+    llmint8_quantize_rows, llmint8_scaled_matmul,
 )

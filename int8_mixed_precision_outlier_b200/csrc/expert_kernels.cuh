@@ -117,8 +117,8 @@ __device__ __forceinline__ void code_chunk(const Chunk& k, float s, float inv, u
 // codes; VPT = 0: read again (from L1 or L2).  Without positions row t goes to
 // row t; with them, to every row positions[t * copies + j] >= 0.
 //
-// Bound by memory; 40 registers keep 1536 threads on an SM (72 took 33 us for
-// 4096 x 8192 fp16).
+// Bound by memory: 4096 x 8192 fp16 takes 22.5 us (4.5 TB/s, the codes staying
+// in L2); 40 registers keep 1536 threads on an SM (with 72 it took 33 us).
 template <int IT, int VPT>
 __global__ void __maxnreg__(40)
     quantize_rows_kernel(const void* X, int K, const int32_t* positions, int copies, int S, int8_t* Xq,
@@ -207,8 +207,8 @@ __global__ void __maxnreg__(40)
 // atomics: the result does not depend on timing.
 //
 // Bound by latency: the ids are loaded once, all in flight, and stay in
-// registers with their ranks (65536 choices of 128 experts: 19.7 us with a
-// second pass over the ids).  ITEMS > 0: at most ITEMS ids a lane.  ITEMS = 0:
+// registers with their ranks (65536 choices of 128 experts: 11.4 us, 19.7 with
+// a second pass over the ids).  ITEMS > 0: at most ITEMS ids a lane.  ITEMS = 0:
 // any number; the ranks wait in `positions` and the ids are read again.
 constexpr int kPosThreads = 1024;
 constexpr int kPosWarps = kPosThreads / 32;
@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(kPosThreads, 1)
 //   out[t, n] = sum_j weights[t, j] * Y[positions[t, j], n]
 // over the j with a position, in binary32 and ascending j (one order, so the
 // result does not depend on timing), rounded once.  Y's rows are read once
-// and 16 bytes at a time where N and the types allow.
+// and 16 bytes at a time where N and the types allow.  Bound by memory: 4096
+// tokens of 4 rows of 5120, bf16, take 36.5 us (5.7 TB/s).
 constexpr int kCombineThreads = 128;
 
 template <int T>

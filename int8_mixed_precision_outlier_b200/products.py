@@ -141,7 +141,7 @@ def _launch_quantize(X, positions, Xq, xscale, S, st):
         xscale = torch.empty(S, dtype=_F32, device=X.device)
     at, copies = (None, 0) if positions is None else (positions.data_ptr(), positions.shape[1])
     rc = _lib().llmint8_quantize_rows(X.data_ptr(), _DTYPES[X.dtype], T, K, at, copies, S, Xq.data_ptr(),
-                                              xscale.data_ptr(), st)
+                                      xscale.data_ptr(), st)
     if rc:
         _check(rc, "llmint8_quantize_rows")
     return Xq, xscale
@@ -283,7 +283,7 @@ def _launch_positions(ids, experts, positions, offsets, st):
     if offsets is None:
         offsets = torch.empty(experts + 1, dtype=_I32, device=ids.device)
     rc = _lib().llmint8_expert_positions(ids.data_ptr(), 8 if ids.dtype is _I64 else 4, T, k, experts,
-                                                 positions.data_ptr(), offsets.data_ptr(), st)
+                                         positions.data_ptr(), offsets.data_ptr(), st)
     if rc:
         _check(rc, "llmint8_expert_positions")
     return positions, offsets
@@ -333,7 +333,7 @@ def _launch_combine(Y, positions, weights, dtype, out, st):
     if out is None:
         out = torch.empty(T, N, dtype=dtype, device=Y.device)
     rc = _lib().llmint8_expert_combine(Y.data_ptr(), _DTYPES[Y.dtype], S, N, positions.data_ptr(),
-                                               weights.data_ptr(), T, k, out.data_ptr(), _DTYPES[dtype], st)
+                                       weights.data_ptr(), T, k, out.data_ptr(), _DTYPES[dtype], st)
     if rc:
         _check(rc, "llmint8_expert_combine")
     return out
