@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool issuer = elect_one();
     previous_done();
     int s = 0;              // the stage to fill next
-    uint32_t phase = 1;     // parity its `empty` barrier had before this round (passes at once in round 0)
+    uint32_t phase = 1;     // parity its `empty` barrier had on the lap before (passes at once on lap 0)
     bool ok = true;
     int i = 0;
     for (Tile t, t2; ok && take(i, t);) {

@@ -361,6 +361,8 @@ class Int8Experts:
             raise ValueError(f"W1 must be [E, 2 F, K] and W2 [E, N, F], got {tuple(W1.shape)} and {tuple(W2.shape)}")
         self.E, two_f, self.K = W1.shape
         self.N, self.F = W2.shape[1:]
+        if not 1 <= self.E <= MAX_EXPERTS:
+            raise ValueError(f"experts must be in [1, {MAX_EXPERTS}], got {self.E}")
         if self.K % 16 or self.F % 16:
             raise ValueError(f"K and F must be multiples of 16, got {self.K} and {self.F}")
         q, s = llmint8_quantize_rows(W1.reshape(-1, self.K).contiguous())

@@ -113,6 +113,18 @@ def test_binding_refuses_host_tensors():
         L.llmint8_expert_positions(torch.zeros(2, 2), 4)
 
 
+def test_int8_experts_refuses_at_construction():
+    """Shapes that no call could use are refused before anything is quantised."""
+    for E in (0, 1025):
+        with pytest.raises(ValueError, match="experts"):
+            L.Int8Experts(torch.zeros(E, 32, 16), torch.zeros(E, 16, 16))
+    for w1, w2 in [((2, 32, 24), (2, 16, 16)), ((2, 24, 16), (2, 16, 12))]:
+        with pytest.raises(ValueError, match="multiples of 16"):
+            L.Int8Experts(torch.zeros(w1), torch.zeros(w2))
+    with pytest.raises(ValueError, match="W1 must be"):
+        L.Int8Experts(torch.zeros(2, 32, 16), torch.zeros(3, 16, 16))
+
+
 # ------------------------------------------------------------------ index arithmetic, restated
 
 def scan_groups(offsets, S, BT, nN):
