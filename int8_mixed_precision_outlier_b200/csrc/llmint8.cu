@@ -41,6 +41,7 @@ struct DeviceInfo {
   int status = LLMINT8_OK;
   int num_sms = 0;
   int max_pairs = 0;  // 2-CTA clusters of gemm_pair_kernel resident at once
+  int l2_bytes = 0;
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -110,7 +111,7 @@ cudaError_t set_product_attributes() {
   return e;
 }
 
-int device_info(int* num_sms, int* max_pairs = nullptr) {
+int device_info(int* num_sms, int* max_pairs = nullptr, int* l2_bytes = nullptr) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return LLMINT8_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return LLMINT8_ERR_CUDA;
@@ -119,7 +120,8 @@ int device_info(int* num_sms, int* max_pairs = nullptr) {
     int major = 0, minor = 0, sms = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d.l2_bytes, cudaDevAttrL2CacheSize, dev) != cudaSuccess) {
       d.status = LLMINT8_ERR_CUDA;
       return;
     }
@@ -156,6 +158,7 @@ int device_info(int* num_sms, int* max_pairs = nullptr) {
   });
   if (num_sms) *num_sms = d.num_sms;
   if (max_pairs) *max_pairs = d.max_pairs;
+  if (l2_bytes) *l2_bytes = d.l2_bytes;
   return d.status;
 }
 
@@ -757,8 +760,8 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || misaligned4(sx) || misaligned4(sw) ||
       misaligned4(bias) || misaligned4(offsets))
     return LLMINT8_ERR_ALIGNMENT;
-  int max_pairs = 0;
-  const int rc = device_info(nullptr, &max_pairs);
+  int max_pairs = 0, l2_bytes = 0;
+  const int rc = device_info(nullptr, &max_pairs, &l2_bytes);
   if (rc != LLMINT8_OK) return rc;
   const ProductPlan plan = plan_product(static_cast<int>(S), static_cast<int>(N), static_cast<int>(K),
                                         static_cast<int>(E), grouped, gated != 0, max_pairs);
@@ -781,6 +784,7 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   p.mt = grouped ? 0 : product::token_tiles(p.S, p.count);
   p.per = product::tile_rows(p.S, p.mt, plan.BT);
   p.mt >>= plan.wide;
+  p.drop = static_cast<double>(E) * static_cast<double>(N) * static_cast<double>(K) > l2_bytes;
   p.quarter = plan.quarter;
   p.b_rows = plan.b_rows;
   p.stages = plan.stages;

@@ -25,7 +25,7 @@
 // 256-column accumulators let the next tile's products run while the epilogue
 // drains the last one.  Every mbarrier wait is bounded.
 //
-// Few tokens are bound by reading the weights (1 x 11008 x 4096: 10.7 us, 45 MB
+// Few tokens are bound by reading the weights (1 x 11008 x 4096: 10.6 us, 45 MB
 // at 4.2 TB/s with the launch and the last tiles in it), many by the tensor
 // cores and the copies of the operands from L2 (4096 x 28672 x 8192: 567 us,
 // 3.4 POP/s; 661 us sustained, at the card's 1000 W).
@@ -95,6 +95,7 @@ struct Params {
   int BT;              // most tokens of a tile, a multiple of 16
   int mt, per;         // without offsets: token tiles, rows of each (of each half, where they have two)
   TileCount count;     // of BT
+  int drop;            // 1: weights that one tile alone reads leave L2 first
   int quarter;         // token rows of a copy come in 1..4 quarters (a multiple of 8 rows each)
   int b_rows;          // token rows that a k-block of a stage has room for
   int stages;
@@ -190,10 +191,11 @@ struct Walk {
       search(p, s);
     }
   }
-  // Group, tile along the channels, first row of Xq / Y, rows; `half` 0 or 1 of a tile of two.
-  __device__ int4 tile(bool wide, int half) const {
-    const int at = ((i << wide) + half) * per;
-    return make_int4(g, nt, begin + at, min(per, rows - at));
+  // Group, tile along the channels, first row of Xq / Y, rows (negative where the
+  // weights leave L2 first); `half` 0 or 1 of a tile of two.
+  __device__ int4 tile(const Params& p, bool wide, int half) const {
+    const int at = ((i << wide) + half) * per, tokens = min(per, rows - at);
+    return make_int4(g, nt, begin + at, p.drop && mt == 1 ? -tokens : tokens);
   }
 };
 
@@ -467,12 +469,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   // the end (or when the wait ran out).
   struct Tile {
     int g, nt, row, tokens;  // group, tile along the channels, first row of Xq / Y, rows
+    bool drop;               // its weights leave L2 first
   };
   auto take = [&](int& i, Tile& t) {
     const int slot = i % AHEAD;
     const bool ok = all_wait(&planned[slot], (i / AHEAD) & 1, kErrTimeoutProducer);
     const int4 v = tiles[slot];
-    t = Tile{v.x, v.y, v.z, v.w};
+    t = Tile{v.x, v.y, v.z, abs(v.w), v.w < 0};
     __syncwarp();  // all lanes have read
     if (lane == 0) mbar_arrive(&taken[slot]);
     ++i;
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = i < AHEAD || all_wait(&taken[slot], ((i / AHEAD) & 1) ^ 1, kErrTimeoutProducer);
       const bool more = ok && t.more();
       if (lane == 0) {
-        tiles[slot] = more ? t.tile(WIDE, half) : make_int4(-1, 0, 0, 0);
+        tiles[slot] = more ? t.tile(p, WIDE, half) : make_int4(-1, 0, 0, 0);
         mbar_arrive(&planned[slot]);
       }
       __syncwarp();
@@ -510,6 +513,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     // then uniform values.  (With the loop inside `if (lane == 0)` an MMA took
     // 71 cycles to issue and a stage 300 more, whatever its size.)
     const bool issuer = elect_one();
+    // Weights that no other tile reads, of a call whose weights are more than L2
+    // holds (none would be there at the next call), leave L2 first: 256 tokens
+    // to 4 of 32 experts of 4096 x 2048 take 44.3 us, 47.7 without; 500 to 2 of 8
+    // of 8192 x 4096 48.6 and 51.6; 150 x 27648 x 5120 28.8 and 29.9.  (Where a
+    // group has several tiles it costs 1 to 3 %, for smaller weights that would
+    // have stayed, 64 x 4096 x 4096, 1.2 us of 6.6.)
+    const uint64_t first_out = policy_evict_first();
     previous_done();
     int s = 0;              // the stage to fill next
     uint32_t phase = 1;     // parity its `empty` barrier had on the lap before (passes at once on lap 0)
@@ -532,10 +542,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int kb = p.ksplit ? u * p.KPB : 0, x = p.ksplit ? 0 : u * BK;
           const uint32_t bar = map_shared_rank(&full[s], 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
-          if constexpr (GATED)
-            tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.g, wt * (p.H / 32), kb);
-          else
-            tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.g);
+          if constexpr (GATED) {
+            if (t.drop)
+              tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.g, wt * (p.H / 32), kb, first_out);
+            else
+              tma_load_5d_pair(stage_a(s), &tmap_w, bar, x, 0, 2 * t.g, wt * (p.H / 32), kb);
+          } else {
+            if (t.drop)
+              tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.g, first_out);
+            else
+              tma_load_4d_pair(stage_a(s), &tmap_w, bar, x, wt * p.H, kb, t.g);
+          }
           tma_load_3d_pair(stage_b(s), tmap_x, bar, x, x0, kb);
           if constexpr (WIDE) tma_load_3d_pair(stage_b(s) + half_bytes, &tmaps_x.m[quarters2 - 1], bar, x, x2, kb);
         }
