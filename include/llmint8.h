@@ -372,6 +372,26 @@ LLMINT8_API int llmint8_grouped_matmul(const int8_t* Xq, const float* xscale, in
                                        const float* bias, int64_t N, int gated, void* Y, int dtype, void* stream);
 
 /*
+ * How a product of these sizes is cut (host arithmetic alone, no device is
+ * touched), for tests and measurements.  `pairs`: CTA pairs that run at once;
+ * E = 1 unless grouped.  plan int64 [10] on the host: weight rows of a tile and
+ * CTA, tiles along the channels, most tokens of a tile (of a half), halves (1
+ * or 2), token rows of a quarter copy, token rows that a k-block has room for,
+ * k-blocks per stage, stages, an upper bound of the tiles, 1 where weights that
+ * one tile alone reads leave L2 first.
+ */
+LLMINT8_API int llmint8_product_plan_debug(int64_t S, int64_t N, int64_t K, int64_t E, int grouped, int gated,
+                                           int pairs, int64_t l2_bytes, int64_t* plan);
+
+/*
+ * How `rows` rows of one group are cut into tiles of at most `most`, which
+ * copies of quarters of `quarter` rows bring: tiles int32 [4] on the host = the
+ * tiles, the rows of each, and of the last one the columns of its products and
+ * the quarters that each CTA copies.
+ */
+LLMINT8_API int llmint8_product_tiles_debug(int64_t rows, int most, int quarter, int32_t* tiles);
+
+/*
  * The order of a router's choices by expert, stable in the order of ids [T][k]
  * (id_bytes 4 or 8: signed integers):
  *   offsets int32 [E+1]: expert e's rows begin at offsets[e]; offsets[E] = rows

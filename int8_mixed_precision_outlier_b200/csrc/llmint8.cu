@@ -660,10 +660,11 @@ bool float_dtype(int d) { return d == LLMINT8_F16 || d == LLMINT8_BF16 || d == L
 struct ProductPlan {
   int BT = 0, quarter = 0, b_rows = 0, KPB = 0, H = 0, stages = 0, nN = 0;
   bool wide = false;  // tiles of two halves of BT tokens
+  bool drop = false;  // weights that one tile alone reads leave L2 first
   int64_t tiles = 0;  // an upper bound
 };
 
-ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, int max_pairs) {
+ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, int max_pairs, int64_t l2_bytes) {
   const int groups = grouped ? std::min(E, S) : 1;
   const int64_t avg = (static_cast<int64_t>(S) + groups - 1) / groups;  // tokens of a group
   const bool ksplit = K % product::BK == 0;
@@ -744,17 +745,25 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   while (ksplit && best.KPB < wish && 2 * best.KPB <= KB && 4 * 2 * best.KPB * kblock <= product::RING_BYTES)
     best.KPB *= 2;
   best.stages = std::min(product::MAX_STAGES, product::RING_BYTES / (kblock * best.KPB));
+  best.drop = static_cast<double>(E) * static_cast<double>(N) * static_cast<double>(K) > static_cast<double>(l2_bytes);
   return best;
+}
+
+// Sizes and flags of a product, before any pointer is looked at.
+int product_sizes(int64_t S, int64_t N, int64_t K, int64_t E, int gated) {
+  if (S < 0 || N < 0 || S > INT32_MAX - product::MAX_BT || N > INT32_MAX - 2 * product::BM || K < 16 || K > kMaxK)
+    return LLMINT8_ERR_INVALID_ARG;
+  if (E < 1 || E > product::MAX_GROUPS) return LLMINT8_ERR_INVALID_ARG;
+  if (gated && N % 32 != 0) return LLMINT8_ERR_INVALID_ARG;
+  return K % 16 != 0 ? LLMINT8_ERR_ALIGNMENT : LLMINT8_OK;
 }
 
 int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const int32_t* offsets, bool grouped,
                  int64_t E, const int8_t* Wq, const float* sw, const float* bias, int64_t N, int gated, void* Y,
                  int dtype, void* stream) {
-  if (S < 0 || N < 0 || S > INT32_MAX - product::MAX_BT || N > INT32_MAX - 2 * product::BM || K < 16 || K > kMaxK)
-    return LLMINT8_ERR_INVALID_ARG;
-  if (E < 1 || E > product::MAX_GROUPS || !float_dtype(dtype)) return LLMINT8_ERR_INVALID_ARG;
-  if (gated && N % 32 != 0) return LLMINT8_ERR_INVALID_ARG;
-  if (K % 16 != 0) return LLMINT8_ERR_ALIGNMENT;
+  if (!float_dtype(dtype)) return LLMINT8_ERR_INVALID_ARG;
+  const int sizes = product_sizes(S, N, K, E, gated);
+  if (sizes != LLMINT8_OK) return sizes;
   if (S == 0 || N == 0) return LLMINT8_OK;
   if (!Xq || !sx || !Wq || !sw || !Y || (grouped && !offsets)) return LLMINT8_ERR_INVALID_ARG;
   if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || misaligned4(sx) || misaligned4(sw) ||
@@ -764,7 +773,7 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   const int rc = device_info(nullptr, &max_pairs, &l2_bytes);
   if (rc != LLMINT8_OK) return rc;
   const ProductPlan plan = plan_product(static_cast<int>(S), static_cast<int>(N), static_cast<int>(K),
-                                        static_cast<int>(E), grouped, gated != 0, max_pairs);
+                                        static_cast<int>(E), grouped, gated != 0, max_pairs, l2_bytes);
   if (plan.tiles > INT32_MAX - 4096) return LLMINT8_ERR_INVALID_ARG;
   product::Params p;
   p.S = static_cast<int>(S);
@@ -784,7 +793,7 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   p.mt = grouped ? 0 : product::token_tiles(p.S, p.count);
   p.per = product::tile_rows(p.S, p.mt, plan.BT);
   p.mt >>= plan.wide;
-  p.drop = static_cast<double>(E) * static_cast<double>(N) * static_cast<double>(K) > l2_bytes;
+  p.drop = plan.drop;
   p.quarter = plan.quarter;
   p.b_rows = plan.b_rows;
   p.stages = plan.stages;
@@ -1276,6 +1285,30 @@ int llmint8_grouped_matmul(const int8_t* Xq, const float* xscale, int64_t S, int
                            int64_t E, const int8_t* Wq, const float* Wscale, const float* bias, int64_t N, int gated,
                            void* Y, int dtype, void* stream) {
   return product_impl(Xq, xscale, S, K, offsets, true, E, Wq, Wscale, bias, N, gated, Y, dtype, stream);
+}
+
+int llmint8_product_plan_debug(int64_t S, int64_t N, int64_t K, int64_t E, int grouped, int gated, int pairs,
+                               int64_t l2_bytes, int64_t* plan) {
+  const int rc = product_sizes(S, N, K, E, gated);
+  if (rc != LLMINT8_OK) return rc;
+  if (S == 0 || N == 0 || pairs < 1 || (!grouped && E != 1) || !plan) return LLMINT8_ERR_INVALID_ARG;
+  const ProductPlan p = plan_product(static_cast<int>(S), static_cast<int>(N), static_cast<int>(K),
+                                     static_cast<int>(E), grouped != 0, gated != 0, pairs, l2_bytes);
+  const int64_t out[10] = {p.H, p.nN, p.BT, p.wide ? 2 : 1, p.quarter, p.b_rows, p.KPB, p.stages, p.tiles, p.drop};
+  std::copy(out, out + 10, plan);
+  return LLMINT8_OK;
+}
+
+int llmint8_product_tiles_debug(int64_t rows, int most, int quarter, int32_t* tiles) {
+  if (rows < 1 || rows > INT32_MAX - product::MAX_BT || most < 16 || most > product::MAX_BT || most % 16 != 0 ||
+      quarter < 8 || !tiles)
+    return LLMINT8_ERR_INVALID_ARG;
+  const int m = static_cast<int>(rows), mt = product::token_tiles(m, product::tile_count(most));
+  const int per = product::tile_rows(m, mt, most);
+  const int last = product::mma_columns(static_cast<int>(rows - static_cast<int64_t>(per) * (mt - 1)));
+  const int32_t out[4] = {mt, per, last, product::quarters_of(quarter, last / 2)};
+  std::copy(out, out + 4, tiles);
+  return LLMINT8_OK;
 }
 
 int llmint8_expert_positions(const void* ids, int id_bytes, int64_t T, int64_t k, int64_t E, int32_t* positions,

@@ -124,6 +124,15 @@ __host__ __device__ inline int tile_rows(int m, int mt, int bt) {
   return per;
 }
 
+// Columns (the MMA's N) of the products of a tile of `tokens` rows.  Each CTA
+// of the pair copies half as many token rows.
+__host__ __device__ inline int mma_columns(int tokens) { return (tokens + 15) / 16 * 16; }
+
+// Quarters that hold `rows` token rows (1..4).
+__host__ __device__ inline int quarters_of(int quarter, int rows) {
+  return 1 + (rows > quarter) + (rows > 2 * quarter) + (rows > 3 * quarter);
+}
+
 // The groups, in shared memory.
 struct Groups {
   int* off;        // [E + 1] rows
@@ -365,11 +374,6 @@ struct Epilogue {
   }
 };
 
-// Quarters that hold `rows` token rows (1..4).
-__device__ __forceinline__ int quarters_of(const Params& p, int rows) {
-  return 1 + (rows > p.quarter) + (rows > 2 * p.quarter) + (rows > 3 * p.quarter);
-}
-
 // GATED: the weight copies interleave 16 gate rows with the 16 value rows of
 // the same channels, so that lanes l and l + 16 of a warp hold the two halves
 // of one output.  OT: output type.
@@ -527,13 +531,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     int i = 0;
     for (Tile t, t2; ok && take(i, t);) {
       if (WIDE && !take(i, t2)) break;
-      const int mine = (t.tokens + 15) / 16 * 8;  // token rows this CTA copies: half the MMA's N
+      const int mine = mma_columns(t.tokens) / 2;  // token rows this CTA copies
       const int wt = 2 * t.nt + rank;             // this CTA's weight rows, in units of H
       const int x0 = t.row + rank * mine;
-      const int quarters = quarters_of(p, mine);
+      const int quarters = quarters_of(p.quarter, mine);
       const CUtensorMap* tmap_x = &tmaps_x.m[quarters - 1];
-      const int mine2 = WIDE ? (t2.tokens + 15) / 16 * 8 : 0, x2 = WIDE ? t2.row + rank * mine2 : 0;
-      const int quarters2 = WIDE ? quarters_of(p, mine2) : 0;
+      const int mine2 = WIDE ? mma_columns(t2.tokens) / 2 : 0, x2 = WIDE ? t2.row + rank * mine2 : 0;
+      const int quarters2 = WIDE ? quarters_of(p.quarter, mine2) : 0;
       const uint32_t tx = static_cast<uint32_t>(2 * p.KPB * (a_bytes + (quarters + quarters2) * p.quarter * BK));
       for (int u = 0; u < p.NU; ++u) {
         ok = mbar_wait_stage(&empty[s], phase, p.wait_ns, kErrTimeoutProducer);
@@ -579,13 +583,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       int i = 0;
       for (Tile t, t2; ok && take(i, t); tc += 1 + WIDE) {
         if (WIDE && !take(i, t2)) break;
-        const int cols = (t.tokens + 15) / 16 * 16;
+        const int cols = mma_columns(t.tokens);
         const uint32_t idesc = idesc_i8_s32(2 * BM, cols);
         // k-blocks of a stage lie as the copy put them: its rows apart
-        const uint32_t b_step = static_cast<uint32_t>(quarters_of(p, cols / 2) * p.quarter * BK) >> 4;
-        const int cols2 = WIDE ? (t2.tokens + 15) / 16 * 16 : 0;
+        const uint32_t b_step = static_cast<uint32_t>(quarters_of(p.quarter, cols / 2) * p.quarter * BK) >> 4;
+        const int cols2 = WIDE ? mma_columns(t2.tokens) : 0;
         const uint32_t idesc2 = idesc_i8_s32(2 * BM, WIDE ? cols2 : 16);
-        const uint32_t b_step2 = static_cast<uint32_t>(quarters_of(p, cols2 / 2) * p.quarter * BK) >> 4;
+        const uint32_t b_step2 = static_cast<uint32_t>(quarters_of(p.quarter, cols2 / 2) * p.quarter * BK) >> 4;
         const int buf = tc & 1;
         if (tc >= 2) {
           ok = __all_sync(0xffffffffu,
