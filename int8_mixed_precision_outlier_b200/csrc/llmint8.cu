@@ -669,7 +669,9 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   const int64_t avg = (static_cast<int64_t>(S) + groups - 1) / groups;  // tokens of a group
   const bool ksplit = K % product::BK == 0;
   const int KB = (K + product::BK - 1) / product::BK;
-  auto up16 = [](int64_t x) { return static_cast<int>((x + 15) / 16 * 16); };
+  auto columns = [](int64_t x) {
+    return static_cast<int>((x + product::COL_STEP - 1) / product::COL_STEP * product::COL_STEP);
+  };
   ProductPlan best;
   // A CTA pair runs its tiles one after the other, `rounds` in all; a tile
   // costs KB steps.  A step was measured at 0.04 us + 1.04 ns a token column
@@ -684,7 +686,7 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
     const double tiles = static_cast<double>(groups) * static_cast<double>(mt) * nN / max_pairs;
     // many tiles of different lengths even out
     const double rounds = grouped && tiles > 4.0 ? tiles : std::ceil(tiles);
-    const int cols = up16((avg + mt - 1) / mt);
+    const int cols = columns((avg + mt - 1) / mt);
     const double cost =
         rounds * (KB * (0.04 + 0.00104 * std::max(cols, 64) + 0.0004 * std::max(H, 64)) + 0.5) + 0.006 * cols +
         0.7 * std::min(tiles, 1.0);
@@ -700,12 +702,12 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
     const int nN = static_cast<int>((static_cast<int64_t>(N) + 2 * H - 1) / (2 * H));
     if (grouped) {
       // room for groups twice as long as the average without a second tile
-      const int BT = std::min(product::MAX_BT, up16(std::min<int64_t>(2 * avg, product::MAX_BT) + 16));
+      const int BT = std::min(product::MAX_BT, columns(std::min<int64_t>(2 * avg, product::MAX_BT) + 16));
       consider(H, nN, BT, (avg + BT - 1) / BT);
     } else {
       const int64_t least = (avg + product::MAX_BT - 1) / product::MAX_BT;
       for (int64_t mt = least; mt <= least + 8 && (mt == least || avg > 32 * (mt - 1)); ++mt)
-        consider(H, nN, up16((avg + mt - 1) / mt), mt);
+        consider(H, nN, columns((avg + mt - 1) / mt), mt);
     }
   }
   best.tiles = (static_cast<int64_t>(S) / best.BT + groups) * best.nN;
@@ -719,7 +721,7 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   if (!grouped && avg > product::MAX_BT) {
     const int H = product::BM, nN = static_cast<int>((static_cast<int64_t>(N) + 2 * H - 1) / (2 * H));
     const int64_t wide = (avg + 2 * product::MAX_BT - 1) / (2 * product::MAX_BT);
-    const int half = up16((avg + 2 * wide - 1) / (2 * wide));
+    const int half = columns((avg + 2 * wide - 1) / (2 * wide));
     const double rounds = std::ceil(static_cast<double>(wide) * nN / max_pairs);
     const double cost = rounds * (KB * (0.04 + 0.00104 * 2 * half + 0.0004 * H) + 0.5 + 0.006 * 2 * half) +
                         0.7 * std::min(static_cast<double>(wide) * nN / max_pairs, 1.0);
@@ -738,7 +740,7 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   // its products 2 a token column and k-block (160 at least), so stages of
   // narrow tiles hold more; four stages at least, or the loads wait.
   // 16 x 4096 x 4096: 11.1, 8.2, 7.3 us with 1, 2, 4 k-blocks.
-  const int cols = std::min(best.BT << best.wide, up16(avg));
+  const int cols = std::min(best.BT << best.wide, columns(avg));
   const int wish = cols >= 224 ? 1 : cols >= 96 ? 2 : product::KPB_MAX;
   const int kblock = (best.H + (best.b_rows << best.wide)) * product::BK;
   best.KPB = 1;
@@ -1300,8 +1302,8 @@ int llmint8_product_plan_debug(int64_t S, int64_t N, int64_t K, int64_t E, int g
 }
 
 int llmint8_product_tiles_debug(int64_t rows, int most, int quarter, int32_t* tiles) {
-  if (rows < 1 || rows > INT32_MAX - product::MAX_BT || most < 16 || most > product::MAX_BT || most % 16 != 0 ||
-      quarter < 8 || !tiles)
+  if (rows < 1 || rows > INT32_MAX - product::MAX_BT || most < product::COL_STEP || most > product::MAX_BT ||
+      most % product::COL_STEP != 0 || quarter < 8 || !tiles)
     return LLMINT8_ERR_INVALID_ARG;
   const int m = static_cast<int>(rows), mt = product::token_tiles(m, product::tile_count(most));
   const int per = product::tile_rows(m, mt, most);

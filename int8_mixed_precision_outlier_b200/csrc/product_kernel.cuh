@@ -12,10 +12,11 @@
 // applied in binary32 and the result is rounded once to the output type.
 //
 // The operands are swapped (A = weight rows, B = token codes): the MMA's
-// M = 128 lanes hold output channels and its N = 16..256 columns hold the
-// tokens of one tile, rounded up to 16.  A group's ragged end so costs at most
-// 15 columns instead of a 128-row tile, and few tokens cost few columns, which
-// leaves short groups bound by reading the weights.
+// M = 128 lanes hold output channels and its N = 32..256 columns hold the
+// tokens of one tile, rounded up to 32 (kind::i8 on a CTA pair takes N in steps
+// of 32).  A group's ragged end so costs at most 31 columns instead of a
+// 128-row tile, and few tokens cost few columns, which leaves short groups
+// bound by reading the weights.
 //
 // One persistent pair of CTAs per two SMs walks the tiles w = unit, + units,
 // ...; tile w belongs to the group whose cumulative tile count covers it, found
@@ -40,6 +41,7 @@ namespace product {
 constexpr int BM = 128;            // MMA M: channels (TMEM lanes) of a tile
 constexpr int BK = 128;            // bytes of K per k-block
 constexpr int MAX_BT = 256;        // most tokens of a tile (MMA N)
+constexpr int COL_STEP = 32;       // N of kind::i8 with cta_group::2: 32, 64, ... 256
 constexpr int KPB_MAX = 4;         // k-blocks per stage
 constexpr int MAX_STAGES = 12;
 constexpr int MAX_GROUPS = 1024;   // 32 * 32: see Walk::search
@@ -65,7 +67,7 @@ static_assert(SX_BYTES + GROUP_BYTES + BAR_BYTES >= BM * BK, "the last stage's 1
 enum : int { kF16 = 0, kBF16 = 1, kF32 = 2 };
 
 // A group of m rows is cut into mt = ceil(m / BT) tiles of `per` rows (a
-// multiple of 16, at most BT; the last tile may be shorter).  BT <= 256 is the
+// multiple of COL_STEP, at most BT; the last tile may be shorter).  BT <= 256 is the
 // same for all, so the division is a multiplication: with `shift` = 31 +
 // ceil(log2 BT) and magic = floor(2^shift / BT) + 1, the product x * magic of
 // x = m + BT - 1 < 2^31 exceeds 2^shift x / BT by at most x < 2^shift / BT, so
@@ -92,7 +94,7 @@ struct Params {
   int ksplit;          // 1: the copies see K as [K / 128][128] (K % 128 == 0); 0: as one row, KPB = 1
   int H;               // weight rows of a tile and CTA (a multiple of 8; of 32 when gated)
   int nN;              // tiles along the channels (2 H rows each for CTA pairs)
-  int BT;              // most tokens of a tile, a multiple of 16
+  int BT;              // most tokens of a tile, a multiple of COL_STEP
   int mt, per;         // without offsets: token tiles, rows of each (of each half, where they have two)
   TileCount count;     // of BT
   int drop;            // 1: weights that one tile alone reads leave L2 first
@@ -113,20 +115,20 @@ struct TokenMaps {
   CUtensorMap m[4];
 };
 
-// Equal shares up to the rounding to 16; an estimate that falls short of m is
-// raised (BT itself never does).
-__host__ __device__ inline int tile_rows(int m, int mt, int bt) {
-  if (mt <= 1) return (m + 15) / 16 * 16;
-  const int share = static_cast<int>(static_cast<float>(m) / static_cast<float>(mt)) + 1;
-  int per = (share + 15) / 16 * 16;
-  if (per > bt) per = bt;
-  if (static_cast<int64_t>(per) * mt < m) per += 16;
-  return per;
-}
-
 // Columns (the MMA's N) of the products of a tile of `tokens` rows.  Each CTA
 // of the pair copies half as many token rows.
-__host__ __device__ inline int mma_columns(int tokens) { return (tokens + 15) / 16 * 16; }
+__host__ __device__ inline int mma_columns(int tokens) { return (tokens + COL_STEP - 1) / COL_STEP * COL_STEP; }
+
+// Equal shares up to the rounding to COL_STEP; an estimate that falls short of m
+// is raised (BT itself never does).
+__host__ __device__ inline int tile_rows(int m, int mt, int bt) {
+  if (mt <= 1) return mma_columns(m);
+  const int share = static_cast<int>(static_cast<float>(m) / static_cast<float>(mt)) + 1;
+  int per = mma_columns(share);
+  if (per > bt) per = bt;
+  if (static_cast<int64_t>(per) * mt < m) per += COL_STEP;
+  return per;
+}
 
 // Quarters that hold `rows` token rows (1..4).
 __host__ __device__ inline int quarters_of(int quarter, int rows) {
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // k-blocks of a stage lie as the copy put them: its rows apart
         const uint32_t b_step = static_cast<uint32_t>(quarters_of(p.quarter, cols / 2) * p.quarter * BK) >> 4;
         const int cols2 = WIDE ? mma_columns(t2.tokens) : 0;
-        const uint32_t idesc2 = idesc_i8_s32(2 * BM, WIDE ? cols2 : 16);
+        const uint32_t idesc2 = idesc_i8_s32(2 * BM, WIDE ? cols2 : COL_STEP);
         const uint32_t b_step2 = static_cast<uint32_t>(quarters_of(p.quarter, cols2 / 2) * p.quarter * BK) >> 4;
         const int buf = tc & 1;
         if (tc >= 2) {

@@ -108,6 +108,19 @@ def test_tiles_cover_their_group(lib, most):
         assert m - per * (count - 1) <= columns <= most
 
 
+def test_columns_are_a_shape_of_the_pair_product(lib):
+    """kind::i8 on a CTA pair takes N = 32, 64, ... 256 columns: every height of every tile, the last one's too."""
+    for rows in range(1, 257):
+        columns = tiles(lib, rows, 256)[2]
+        assert columns % 32 == 0 and rows <= columns <= 256, rows
+    for S, N, K, E, gated in some_products(4, 600):
+        p = plan(lib, S, N, K, E, gated)
+        assert p.BT % 32 == 0 and 32 <= p.BT <= 256
+        for rows in {S if E is None else max(1, S // E), p.BT + 1, 3 * p.BT - 17}:
+            _, per, columns, _ = tiles(lib, rows, p.BT)
+            assert per % 32 == 0 and columns % 32 == 0, (p, rows)
+
+
 def test_halves_have_rows(lib):
     """A tile of two halves is planned only where each half of each tile has rows."""
     cut = 0
@@ -126,9 +139,9 @@ def test_which_plans_the_tested_shapes_take(lib):
     GPU: a change of the plan's constants may not take one of them away unseen."""
     halves = {s: plan(lib, *s[:3], gated=s[3]).halves for s in
               [(257, 13824, 2048, False), (270, 18944, 2064, True), (600, 9001, 4096, False),
-               (513, 8192, 4112, True), (1213, 18442, 6160, False), (150, 40000, 128, False)]}
+               (513, 8192, 4112, True), (1051, 12297, 8064, False), (150, 40000, 128, False)]}
     assert halves[257, 13824, 2048, False] == 2 and halves[270, 18944, 2064, True] == 2
-    assert halves[1213, 18442, 6160, False] == 2 and halves[150, 40000, 128, False] == 1
+    assert halves[1051, 12297, 8064, False] == 2 and halves[150, 40000, 128, False] == 1
     assert plan(lib, 64, 4096, 512).KPB == 2 and plan(lib, 16, 4096, 4096).KPB == 4 and plan(lib, 33, 257, 272).KPB == 1
     assert plan(lib, 16, 4096, 2048, E=16).drop == 1 and plan(lib, 16, 4096, 2048, E=8).drop == 0
 
