@@ -465,8 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto stage_a = [&](int s) { return smem + s * stage_bytes + (half_bytes << WIDE); };
 
   // A wait of a whole warp with one outcome: lanes that gave up and lanes that
-  // did not would part, and never meet again at a warp-wide step.  (The loops
-  // over the stages have no such step and vote once a tile.)
+  // did not would part, and never meet again at a warp-wide step.
   auto all_wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
     return __all_sync(0xffffffffu, mbar_wait_stage(bar, parity, p.wait_ns, code)) != 0;
   };
@@ -515,9 +514,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
-    // All lanes walk the loop, one issues: its addresses and coordinates are
-    // then uniform values.  (With the loop inside `if (lane == 0)` an MMA took
-    // 71 cycles to issue and a stage 300 more, whatever its size.)
+    // All lanes walk the loop, one waits and issues: its addresses and
+    // coordinates are then uniform values.  (With the loop inside `if (lane ==
+    // 0)` an MMA took 71 cycles to issue and a stage 300 more, whatever its
+    // size.)  The others do not ask the stages' barriers: the one that issues
+    // moves them on alone, and a lane that it left behind would find its phase
+    // gone by and wait for another.
     const bool issuer = elect_one();
     // Weights that no other tile reads, of a call whose weights are more than L2
     // holds (none would be there at the next call), leave L2 first: 256 tokens
@@ -542,9 +544,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int quarters2 = WIDE ? quarters_of(p.quarter, mine2) : 0;
       const uint32_t tx = static_cast<uint32_t>(2 * p.KPB * (a_bytes + (quarters + quarters2) * p.quarter * BK));
       for (int u = 0; u < p.NU; ++u) {
-        ok = mbar_wait_stage(&empty[s], phase, p.wait_ns, kErrTimeoutProducer);
-        if (!ok) break;
-        if (issuer) {
+        if (issuer && ok) ok = mbar_wait_stage(&empty[s], phase, p.wait_ns, kErrTimeoutProducer);
+        if (issuer && ok) {
           const int kb = p.ksplit ? u * p.KPB : 0, x = p.ksplit ? 0 : u * BK;
           const uint32_t bar = map_shared_rank(&full[s], 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
@@ -604,8 +605,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(buf * MAX_BT);
         for (int u = 0; u < p.NU; ++u) {
-          if (!ready) ok = mbar_wait_stage(&full[s], phase, p.wait_ns, kErrTimeoutMma);
-          if (!ok) break;
+          if (issuer && ok && !ready) ok = mbar_wait_stage(&full[s], phase, p.wait_ns, kErrTimeoutMma);
           uint64_t* const freed = &empty[s];
           const uint32_t here = stage;
           stage += stage_step;
@@ -614,10 +614,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             stage = ring;
             phase ^= 1;
           }
-          // Asked now, answered while the products are issued.
-          ready = mbar_ready(&full[s], phase);
-          tc_fence_after();
-          if (issuer) {
+          if (issuer && ok) {
+            // Asked now, answered while the products are issued.
+            ready = mbar_ready(&full[s], phase);
+            tc_fence_after();
             const int nkb = u + 1 < p.NU ? p.KPB : p.KB - u * p.KPB;
             auto products = [&](uint32_t acc, uint32_t blow, uint32_t step, uint32_t id) {
               uint32_t alow = here + a_at, add = u > 0;  // the tile's first product overwrites the accumulator
@@ -703,6 +703,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t row_bytes = static_cast<int64_t>(p.No) * SIZE;
         for (int c0 = set * Epi::CHUNK; c0 < a.tok; c0 += EPI_WARPS / 4 * Epi::CHUNK) {
           uint32_t r[Epi::CHUNK];
+          __syncwarp();  // the lanes' stores may have parted them
           tmem_ld32(addr + c0, r);
           tmem_ld_wait();
           tmem_regs_ready(r);

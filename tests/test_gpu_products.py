@@ -153,6 +153,19 @@ def test_scaled_matmul_is_exact_on_integers(L):
         assert torch.equal(Y, want)
 
 
+@pytest.mark.parametrize("T,N,K", [(33, 24000, 65520), (300, 4000, 65520), (1, 40000, 16400), (600, 9001, 16384)])
+def test_tiles_of_many_laps_of_the_ring(L, T, N, K):
+    """Up to 512 stages a tile and several tiles a pair of SMs: every warp goes round the ring of stages with the one
+    that moves it on.  Unit scales, the sums themselves."""
+    g = gen(K + N)
+    Xq, Wq = codes(g, T, K), codes(g, N, K)
+    one = torch.ones(max(T, N), device="cuda")
+    Y = L.llmint8_scaled_matmul(Xq, one[:T].contiguous(), Wq, one[:N].contiguous(), dtype=torch.float32)
+    x = Xq.double()
+    for n0 in range(0, N, 4000):
+        assert torch.equal(Y[:, n0:n0 + 4000], (x @ Wq[n0:n0 + 4000].double().T).float())
+
+
 def test_scaled_matmul_agrees_with_the_int32_product(L):
     g = gen(5)
     Xq, Wq = codes(g, 190, 1024), codes(g, 320, 1024)
