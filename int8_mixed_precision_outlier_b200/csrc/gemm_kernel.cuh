@@ -447,10 +447,12 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         }
         if (ok) mma_commit_pair(tfull, 0x3);
       }
-      mma_commit_pair(done, 0x3);
+      // The pair's MMAs are complete before both CTAs meet and TMEM is
+      // released.  (The odd CTA would wait here for the whole call, which may
+      // well be longer than one wait.)
+      mma_commit_pair(done, 0x1);
+      mbar_wait(done, 0, p.wait_ns, kErrTimeoutMma);
     }
-    // Both CTAs: the pair's MMAs are complete before TMEM is released.
-    if (lane == 0) mbar_wait(done, 0, p.wait_ns, kErrTimeoutMma);
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int set = (warp - 2) >> 2;                           // 0 or 1

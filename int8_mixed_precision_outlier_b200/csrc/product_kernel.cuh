@@ -640,10 +640,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           if constexpr (WIDE) mma_commit_pair(&tfull[1], 0x3);
         }
       }
-      if (issuer) mma_commit_pair(done, 0x3);
+      // The MMAs (of both CTAs) are complete before the pair meets and TMEM is
+      // released.  The odd CTA, which would wait here for the whole call, does
+      // at that meeting, which has no limit to run out.
+      if (issuer) mma_commit_pair(done, 0x1);
+      mbar_wait_stage(done, 0, p.wait_ns, kErrTimeoutMma);
     }
-    // The MMAs (of both CTAs) are complete before TMEM is released.
-    mbar_wait_stage(done, 0, p.wait_ns, kErrTimeoutMma);
   } else {
     // ------------------------------------------------------------ epilogue
     using Epi = Epilogue<GATED, OT>;

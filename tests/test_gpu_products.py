@@ -166,6 +166,29 @@ def test_tiles_of_many_laps_of_the_ring(L, T, N, K):
         assert torch.equal(Y[:, n0:n0 + 4000], (x @ Wq[n0:n0 + 4000].double().T).float())
 
 
+@pytest.mark.parametrize("call", ["scaled", "int32"])
+def test_a_call_longer_than_the_wait_limit_is_no_timeout(L, call):
+    """The limit bounds each wait: a product of milliseconds whose steps take microseconds runs under a limit of one
+    millisecond."""
+    g = gen(40)
+    T, N, K = 65536, 16384, 4096
+    Xq, Wq, one = codes(g, T, K), codes(g, N, K), torch.ones(T, device="cuda")
+    sw = one[:N].contiguous()
+    run = (lambda: L.llmint8_scaled_matmul(Xq, one, Wq, sw, dtype=torch.float32)) if call == "scaled" else \
+        (lambda: L.llmint8_int8_gemm_i32(Xq, Wq))
+    want = run()
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    L.llmint8_set_wait_limit_ns(1_000_000)
+    try:
+        begin.record()
+        Y = run()
+        end.record()
+        assert L.llmint8_sync_status() == 0
+    finally:
+        L.llmint8_set_wait_limit_ns(2_000_000_000)
+    assert begin.elapsed_time(end) > 1.5 and torch.equal(Y, want)
+
+
 def test_scaled_matmul_agrees_with_the_int32_product(L):
     g = gen(5)
     Xq, Wq = codes(g, 190, 1024), codes(g, 320, 1024)
