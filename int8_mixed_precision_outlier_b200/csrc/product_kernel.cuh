@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   // Neither CTA leaves while the other may still signal its barriers or, after
   // a timeout, copies of the pair may still be landing.
-  if (threadIdx.x == 0 && ld_error_word() != 0) sleep_ns_bounded(20000);
+  if (threadIdx.x == 0 && pipeline_gave_up()) sleep_ns_bounded(20000);
   __syncwarp();
   cluster_sync();
   if (warp == 1) {

@@ -142,9 +142,12 @@ __device__ __forceinline__ bool mbar_wait_stage(uint64_t* bar, uint32_t parity, 
   }
 }
 
-// Current value of the error word (a plain volatile read).
-__device__ __forceinline__ uint32_t ld_error_word() {
-  return *reinterpret_cast<volatile uint32_t*>(&g_error_word);
+// Whether a pipeline gave up a wait since the error word was last cleared (a
+// plain volatile read), so that copies of its may still be landing.  The word's
+// other bits tell of arguments and of no copies.
+__device__ __forceinline__ bool pipeline_gave_up() {
+  constexpr uint32_t kPipeline = kErrTimeoutProducer | kErrTimeoutMma | kErrTimeoutEpilogue;
+  return (*reinterpret_cast<volatile uint32_t*>(&g_error_word) & kPipeline) != 0;
 }
 
 // Sleep for about `ns` nanoseconds of %globaltimer time.

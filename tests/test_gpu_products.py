@@ -408,6 +408,42 @@ def test_positions_outside_are_reported_and_stay_inside(L):
     assert torch.equal(out, torch.stack([Y[0] + Y[3], torch.zeros(64, device="cuda"), Y[2], Y[1]]))
 
 
+@pytest.mark.parametrize("call", ["scaled", "int32"])
+def test_a_recorded_argument_does_not_slow_the_next_calls(L, call):
+    """A position outside stays recorded until the status is read; the products in between run as ever.  After a wait
+    that ran out each would stay 20 us longer, for copies that may still be landing: 100 calls are 2 ms apart then, and
+    a quarter of that is allowed for the clocks."""
+    g = gen(12)
+    Xq, Wq, one = codes(g, 256, 256), codes(g, 256, 256), torch.ones(256, device="cuda")
+    acc = torch.empty(256, 256, dtype=torch.int32, device="cuda")
+    Y = torch.empty(256, 256, device="cuda")
+    run = (lambda: L.llmint8_scaled_matmul(Xq, one, Wq, one, Y=Y)) if call == "scaled" else \
+        (lambda: L.llmint8_int8_gemm_i32(Xq, Wq, acc))
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(100):
+            run()
+
+    def ms():
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        times = []
+        for _ in range(7):
+            begin.record()
+            graph.replay()
+            end.record()
+            torch.cuda.synchronize()
+            times.append(begin.elapsed_time(end))
+        return sorted(times)[3]
+    clear = ms()
+    pos = torch.full((1, 1), -9, dtype=torch.int32, device="cuda")
+    L.llmint8_expert_combine(torch.ones(1, 8, device="cuda"), pos, torch.ones(1, 1, device="cuda"))
+    recorded = ms()
+    assert L.llmint8_sync_status() == -1
+    assert recorded < clear + 0.5, (clear, recorded)
+
+
 # ------------------------------------------------------------------ expert positions
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 8), (7, 3, 5), (512, 2, 8), (1000, 4, 64), (4097, 1, 3),
