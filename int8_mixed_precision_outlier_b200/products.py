@@ -22,10 +22,10 @@ _DTYPES = {_F16: 0, _BF16: 1, _F32: 2}
 MAX_EXPERTS = 1024
 
 _Tensor = torch.Tensor
-# The stream's pointer and the device's index alone: 3 us less than by way of a
-# Stream object.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# _C._cuda_getCurrentRawStream and _cuda_getDevice give the stream's pointer and
+# the device's index alone, 3 us less than by way of a Stream object.  A torch
+# without CUDA has neither, so they are looked up in a call.
+_C = torch._C
 
 
 def _lib():
@@ -69,10 +69,10 @@ def _run(index: int, stream, call):
     """call(pointer of the stream) with the tensors' device and the call's
     stream current, so that an output belongs to the stream that writes it."""
     if stream is None:
-        if index == _current_device():
-            return call(_raw_stream(index))
+        if index == _C._cuda_getDevice():
+            return call(_C._cuda_getCurrentRawStream(index))
         with torch.cuda.device(index):
-            return call(_raw_stream(index))
+            return call(_C._cuda_getCurrentRawStream(index))
     if stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     with torch.cuda.stream(stream):
@@ -108,9 +108,9 @@ def llmint8_quantize_rows(X: torch.Tensor, positions: torch.Tensor | None = None
         fine = False
     if not fine:
         _check_quantize(X, positions, Xq, xscale)
-    if stream is not None or index != _current_device():
+    if stream is not None or index != _C._cuda_getDevice():
         return _run(index, stream, lambda st: _launch_quantize(X, positions, Xq, xscale, S, st))
-    return _launch_quantize(X, positions, Xq, xscale, S, _raw_stream(index))
+    return _launch_quantize(X, positions, Xq, xscale, S, _C._cuda_getCurrentRawStream(index))
 
 
 def _check_quantize(X, positions, Xq, xscale):
@@ -193,10 +193,11 @@ def _product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, stream, whe
         fine = False
     if not fine:
         _check_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y)
-    if stream is not None or index != _current_device():
+    if stream is not None or index != _C._cuda_getDevice():
         return _run(index, stream,
                     lambda st: _launch_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, st, where))
-    return _launch_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, _raw_stream(index), where)
+    return _launch_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y,
+                           _C._cuda_getCurrentRawStream(index), where)
 
 
 def _launch_product(Xq, xscale, offsets, Wq, Wscale, bias, gated, dtype, Y, st, where):
@@ -260,9 +261,9 @@ def llmint8_expert_positions(ids: torch.Tensor, experts: int, positions: torch.T
         fine = False
     if not fine:
         _check_positions(ids, experts, positions, offsets)
-    if stream is not None or index != _current_device():
+    if stream is not None or index != _C._cuda_getDevice():
         return _run(index, stream, lambda st: _launch_positions(ids, experts, positions, offsets, st))
-    return _launch_positions(ids, experts, positions, offsets, _raw_stream(index))
+    return _launch_positions(ids, experts, positions, offsets, _C._cuda_getCurrentRawStream(index))
 
 
 def _check_positions(ids, experts, positions, offsets):
@@ -310,9 +311,9 @@ def llmint8_expert_combine(Y: torch.Tensor, positions: torch.Tensor, weights: to
         fine = False
     if not fine:
         _check_combine(Y, positions, weights, dtype, out)
-    if stream is not None or index != _current_device():
+    if stream is not None or index != _C._cuda_getDevice():
         return _run(index, stream, lambda st: _launch_combine(Y, positions, weights, dtype, out, st))
-    return _launch_combine(Y, positions, weights, dtype, out, _raw_stream(index))
+    return _launch_combine(Y, positions, weights, dtype, out, _C._cuda_getCurrentRawStream(index))
 
 
 def _check_combine(Y, positions, weights, dtype, out):

@@ -2,6 +2,9 @@
 refuse before they touch the device, what the Python binding refuses, and restatements in numpy of the kernels' index
 arithmetic (group bounds, tiles, expert positions)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -111,6 +114,22 @@ def test_binding_refuses_host_tensors():
         L.llmint8_quantize_rows(x.double())
     with pytest.raises(TypeError, match="int32 or int64"):
         L.llmint8_expert_positions(torch.zeros(2, 2), 4)
+
+
+def test_import_on_a_torch_without_cuda():
+    """Such a build has none of torch._C's CUDA functions: the package is imported, and what needs no GPU works."""
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_')]:\n"
+            "    delattr(torch._C, name)\n"
+            "import int8_mixed_precision_outlier_b200 as L\n"
+            "assert 'llmint8_scaled_matmul' in L.header_functions()\n"
+            "try:\n"
+            "    L.llmint8_quantize_rows(torch.zeros(4, 64))\n"
+            "except TypeError as e:\n"
+            "    print('refused:', e)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "refused: X must be a CUDA tensor" in r.stdout, r.stderr
 
 
 def test_int8_experts_refuses_at_construction():
