@@ -392,6 +392,14 @@ LLMINT8_API int llmint8_product_plan_debug(int64_t S, int64_t N, int64_t K, int6
 LLMINT8_API int llmint8_product_tiles_debug(int64_t rows, int most, int quarter, int32_t* tiles);
 
 /*
+ * Which kernels a call has made ready on the current device so far (for tests):
+ * bit 0 the decomposition's, bit 1 the products with token and channel scales,
+ * bit 2 the expert positions.  Each is made ready by the first call that
+ * launches it.  -1 where the device is not one that the library runs on.
+ */
+LLMINT8_API int llmint8_prepared_debug(void);
+
+/*
  * The order of a router's choices by expert, stable in the order of ids [T][k]
  * (id_bytes 4 or 8: signed integers):
  *   offsets int32 [E+1]: expert e's rows begin at offsets[e]; offsets[E] = rows

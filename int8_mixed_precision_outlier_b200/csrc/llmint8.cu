@@ -36,12 +36,21 @@ constexpr int64_t kMaxInt32Sum = 133143; // K * 127 * 127 < 2^31
 std::atomic<uint64_t> g_wait_ns{2000000000ull};
 
 // ------------------------------------------------------------ device facts
+// What some kernels need before their first launch on a device, done by the
+// first call that launches one of them: a user of the others neither waits for
+// their loading nor meets a refusal that concerns them.
+enum Part { kDecomposition, kProducts, kPositions, kParts };
 struct DeviceInfo {
   std::once_flag once;
   int status = LLMINT8_OK;
   int num_sms = 0;
-  int max_pairs = 0;  // 2-CTA clusters of gemm_pair_kernel resident at once
   int l2_bytes = 0;
+  struct {
+    std::once_flag once;
+    int status = LLMINT8_OK;
+    int max_pairs = 0;  // 2-CTA clusters of its persistent kernel resident at once
+    std::atomic<bool> done{false};
+  } part[kParts];
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -86,20 +95,28 @@ ProductKernel product_kernel_for(int dtype, bool wide) {
   return wide ? product_kernel_of<GATED, true>(dtype) : product_kernel_of<GATED, false>(dtype);
 }
 
-// Shared-memory limits of the products with token and channel scales and of
-// the expert positions.
+// Shared-memory limits of the products with token and channel scales.
 cudaError_t set_product_attributes() {
   cudaError_t e = cudaSuccess;
-  auto big = [&](auto kern, int bytes) {
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  auto big = [&](auto kern) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, product::SMEM_BYTES);
   };
   for (const int dtype : {product::kF16, product::kBF16, product::kF32})
     for (const bool wide : {false, true}) {
-      big(product_kernel_for<false>(dtype, wide), product::SMEM_BYTES);
-      big(product_kernel_for<true>(dtype, wide), product::SMEM_BYTES);
+      big(product_kernel_for<false>(dtype, wide));
+      big(product_kernel_for<true>(dtype, wide));
     }
+  return e;
+}
+
+// Shared-memory and cluster limits of the expert positions.
+cudaError_t set_position_attributes() {
+  cudaError_t e = cudaSuccess;
   auto positions = [&](auto kern) {
-    big(kern, expert::pos_smem_bytes(product::MAX_GROUPS));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               expert::pos_smem_bytes(product::MAX_GROUPS));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   };
   positions(expert::expert_positions_kernel<int32_t, 1>);
@@ -111,55 +128,85 @@ cudaError_t set_product_attributes() {
   return e;
 }
 
-int device_info(int* num_sms, int* max_pairs = nullptr, int* l2_bytes = nullptr) {
+// How many pairs of a persistent kernel the device keeps resident (GPCs with
+// an odd number of usable SMs leave one idle).
+template <typename Kernel>
+int resident_pairs(Kernel kern, int threads, int smem_bytes, int sms) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (sms / 2));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem_bytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) {
+    cudaGetLastError();
+    clusters = sms / 2;
+  }
+  return clusters;
+}
+
+// The current device, checked to be one that the library runs on.
+int current_device(DeviceInfo** info) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return LLMINT8_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return LLMINT8_ERR_CUDA;
   DeviceInfo& d = g_dev[dev];
   std::call_once(d.once, [&]() {
-    int major = 0, minor = 0, sms = 0;
+    int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d.l2_bytes, cudaDevAttrL2CacheSize, dev) != cudaSuccess) {
+        cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d.l2_bytes, cudaDevAttrL2CacheSize, dev) != cudaSuccess)
       d.status = LLMINT8_ERR_CUDA;
-      return;
-    }
-    if (major != 10 || minor != 0) {
+    else if (major != 10 || minor != 0)
       d.status = LLMINT8_ERR_UNSUPPORTED_ARCH;
-      return;
-    }
-    if (set_attributes<false>() != cudaSuccess || set_attributes<true>() != cudaSuccess ||
-        set_product_attributes() != cudaSuccess) {
-      d.status = LLMINT8_ERR_CUDA;
-      return;
-    }
-    d.num_sms = sms;
-    // How many pairs the persistent GEMM can keep resident (GPCs with an odd
-    // number of usable SMs leave one idle).
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (sms / 2));
-    cfg.blockDim = dim3(gemm::P_THREADS);
-    cfg.dynamicSmemBytes = gemm::P_SMEM_BYTES;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, gemm::gemm_pair_kernel<false>, &cfg) != cudaSuccess ||
-        clusters < 1) {
-      cudaGetLastError();
-      clusters = sms / 2;
-    }
-    d.max_pairs = clusters;
   });
-  if (num_sms) *num_sms = d.num_sms;
-  if (max_pairs) *max_pairs = d.max_pairs;
-  if (l2_bytes) *l2_bytes = d.l2_bytes;
+  *info = &d;
   return d.status;
+}
+
+// The current device with one part's kernels ready to launch.
+int prepared(Part which, DeviceInfo** info) {
+  const int rc = current_device(info);
+  if (rc != LLMINT8_OK) return rc;
+  DeviceInfo& d = **info;
+  auto& part = d.part[which];
+  std::call_once(part.once, [&]() {
+    cudaError_t e = cudaSuccess;
+    if (which == kDecomposition) {
+      e = set_attributes<false>();
+      if (e == cudaSuccess) e = set_attributes<true>();
+      if (e == cudaSuccess)
+        part.max_pairs =
+            resident_pairs(gemm::gemm_pair_kernel<false>, gemm::P_THREADS, gemm::P_SMEM_BYTES, d.num_sms);
+    } else if (which == kProducts) {
+      e = set_product_attributes();
+      if (e == cudaSuccess)
+        part.max_pairs = resident_pairs(product_kernel_for<false>(product::kF16, false), product::THREADS,
+                                        product::SMEM_BYTES, d.num_sms);
+    } else {
+      e = set_position_attributes();
+    }
+    if (e != cudaSuccess) part.status = LLMINT8_ERR_CUDA;
+    part.done = true;
+  });
+  return part.status;
+}
+
+// The decomposition's kernels (every entry but the products' and the experts').
+int device_info(int* num_sms, int* max_pairs = nullptr) {
+  DeviceInfo* d = nullptr;
+  const int rc = prepared(kDecomposition, &d);
+  if (rc != LLMINT8_OK) return rc;
+  if (num_sms) *num_sms = d->num_sms;
+  if (max_pairs) *max_pairs = d->part[kDecomposition].max_pairs;
+  return LLMINT8_OK;
 }
 
 // ------------------------------------------------------------ tensor maps
@@ -771,11 +818,13 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || misaligned4(sx) || misaligned4(sw) ||
       misaligned4(bias) || misaligned4(offsets))
     return LLMINT8_ERR_ALIGNMENT;
-  int max_pairs = 0, l2_bytes = 0;
-  const int rc = device_info(nullptr, &max_pairs, &l2_bytes);
+  DeviceInfo* device = nullptr;
+  const int rc = prepared(kProducts, &device);
   if (rc != LLMINT8_OK) return rc;
+  const int max_pairs = device->part[kProducts].max_pairs;
   const ProductPlan plan = plan_product(static_cast<int>(S), static_cast<int>(N), static_cast<int>(K),
-                                        static_cast<int>(E), grouped, gated != 0, max_pairs, l2_bytes);
+                                        static_cast<int>(E), grouped, gated != 0, max_pairs,
+                                        device->l2_bytes);
   if (plan.tiles > INT32_MAX - 4096) return LLMINT8_ERR_INVALID_ARG;
   product::Params p;
   p.S = static_cast<int>(S);
@@ -854,7 +903,8 @@ int quantize_rows_impl(const void* X, int dtype, int64_t T, int64_t K, const int
   if (T == 0 || S == 0) return LLMINT8_OK;
   if (!X || !Xq || !xscale) return LLMINT8_ERR_INVALID_ARG;
   if (!aligned16(X) || !aligned16(Xq) || misaligned4(xscale) || misaligned4(positions)) return LLMINT8_ERR_ALIGNMENT;
-  const int rc = device_info(nullptr);
+  DeviceInfo* device = nullptr;
+  const int rc = current_device(&device);
   if (rc != LLMINT8_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int t = static_cast<int>(T), k = static_cast<int>(K), c = static_cast<int>(copies), s = static_cast<int>(S);
@@ -888,7 +938,8 @@ int expert_positions_impl(const void* ids, int id_bytes, int64_t T, int64_t k, i
   if (misaligned4(positions) || misaligned4(offsets) ||
       (reinterpret_cast<uintptr_t>(ids) & static_cast<uintptr_t>(id_bytes - 1)))
     return LLMINT8_ERR_ALIGNMENT;
-  const int rc = device_info(nullptr);
+  DeviceInfo* device = nullptr;
+  const int rc = prepared(kPositions, &device);
   if (rc != LLMINT8_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
@@ -916,7 +967,8 @@ int expert_combine_impl(const void* Y, int y_dtype, int64_t S, int64_t N, const 
   const bool vec = N % 8 == 0;
   const int64_t cols = (N + 8 * expert::kCombineThreads - 1) / (8 * expert::kCombineThreads);
   if (cols > 65535) return LLMINT8_ERR_INVALID_ARG;
-  const int rc = device_info(nullptr);
+  DeviceInfo* device = nullptr;
+  const int rc = current_device(&device);
   if (rc != LLMINT8_OK) return rc;
   auto kern = y_dtype == LLMINT8_F16    ? (vec ? combine_kernel_for<expert::kF16, true>(out_dtype)
                                                : combine_kernel_for<expert::kF16, false>(out_dtype))
@@ -1311,6 +1363,14 @@ int llmint8_product_tiles_debug(int64_t rows, int most, int quarter, int32_t* ti
   const int32_t out[4] = {mt, per, last, product::quarters_of(quarter, last / 2)};
   std::copy(out, out + 4, tiles);
   return LLMINT8_OK;
+}
+
+int llmint8_prepared_debug(void) {
+  DeviceInfo* d = nullptr;
+  if (current_device(&d) != LLMINT8_OK) return -1;
+  int parts = 0;
+  for (int i = 0; i < kParts; ++i) parts |= d->part[i].done << i;
+  return parts;
 }
 
 int llmint8_expert_positions(const void* ids, int id_bytes, int64_t T, int64_t k, int64_t E, int32_t* positions,

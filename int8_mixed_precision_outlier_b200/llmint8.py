@@ -68,6 +68,7 @@ def _declare(lib):
         "llmint8_grouped_matmul": (I, [P, P, I64, I64, P, I64, P, P, P, I64, I, P, I, P]),
         "llmint8_product_plan_debug": (I, [I64, I64, I64, I64, I, I, I, I64, P]),
         "llmint8_product_tiles_debug": (I, [I64, I, I, P]),
+        "llmint8_prepared_debug": (I, []),
         "llmint8_expert_positions": (I, [P, I, I64, I64, I64, P, P, P]),
         "llmint8_expert_combine": (I, [P, I, I64, I64, P, P, I64, I64, P, I, P]),
         "llmint8_sync_status": (I, [P]),

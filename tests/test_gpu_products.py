@@ -8,6 +8,10 @@ type.  The int32 sums are exact.
   reciprocal (1 ulp, 2 u) and two products one rounding each: dy <= 1.1 dg |u| + |silu(g)| du + 10 u |y|;
   the output's own rounding: eps / 2 |y|, or half the smallest subnormal step.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -725,6 +729,38 @@ def test_refusals(L):
         with pytest.raises(ValueError):
             L.llmint8_expert_positions(pos, experts)
     torch.cuda.synchronize()
+
+
+CALLS = {
+    "decomposition": "L.llmint8_quantize_weight(torch.ones(8, 64, device='cuda').half())",
+    "product": "L.llmint8_scaled_matmul(q, s, q, s)",
+    "positions": "L.llmint8_expert_positions(torch.zeros(4, 2, dtype=torch.int32, device='cuda'), 4)",
+    "quantize": "L.llmint8_quantize_rows(torch.ones(8, 64, device='cuda'))",
+    "combine": "L.llmint8_expert_combine(torch.ones(8, 64, device='cuda'), torch.zeros(4, 2, dtype=torch.int32, "
+               "device='cuda'), torch.ones(4, 2, device='cuda'))",
+}
+
+
+@pytest.mark.parametrize("order,parts", [(["decomposition"], 1), (["product"], 2), (["positions"], 4),
+                                         (["quantize", "combine"], 0), (["decomposition", "product", "positions"], 7)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_call_makes_its_own_kernels_ready(order, parts, captured):
+    """In a process of its own: the kernels of other calls are neither loaded nor set up, and a first call may be one
+    that is captured."""
+    body = "".join(f"    keep.append({CALLS[c]})\n" for c in order)
+    code = ("import torch, contextlib\nimport int8_mixed_precision_outlier_b200 as L\n"
+            "q, s, keep = torch.ones(8, 64, dtype=torch.int8, device='cuda'), torch.ones(8, device='cuda'), []\n"
+            "torch.cuda.synchronize()\n"
+            "graph = torch.cuda.CUDAGraph()\n"
+            f"with torch.cuda.graph(graph) if {captured} else contextlib.nullcontext():\n{body}"
+            f"if {captured}:\n    graph.replay()\n"
+            "assert L.llmint8_sync_status() == 0\n"
+            f"assert L.load_library().llmint8_prepared_debug() == {parts}, L.load_library().llmint8_prepared_debug()\n"
+            f"if 'product' in {order}:\n"
+            f"    assert (keep[{order}.index('product')] == 64).all()\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
 
 
 def test_empty_calls(L):
