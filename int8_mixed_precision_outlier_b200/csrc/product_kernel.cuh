@@ -269,25 +269,27 @@ __device__ __forceinline__ void scan_groups(const Params& p, const Groups& s) {
   if (bad && blockIdx.x == 0) atomicOr(&g_error_word, kErrBadIndex);
 }
 
-// silu(g) * u = g u / (1 + e^-g) in binary32.  e^-g = 2^h (1 + l ln 2) with
-// h + l = -g log2 e: h is the rounded product, l its error and the part of
-// log2 e that binary32 drops (a constant in two parts, as Cody and Waite's), so
-// the error of h does not grow with g.  ex2 is
-// within 2 ulp and rcp within 1; with the other roundings the result is within
-// 10 * 2^-24 of |silu(g) u| plus what the arguments' errors make.  Below g =
-// -126 ln 2 rcp flushes its result and silu is 0 (it is above -88 * 2^-126
-// there).
+// silu(g) * u in binary32, by t = e^-|g|, which neither overflows nor leaves a
+// flushed reciprocal: g u / (1 + t) for g >= 0, g t u / (1 + t) below.
+// t = 2^h (1 + l ln 2) with h + l = -|g| log2 e: h is the rounded product, l its
+// error and the part of log2 e that binary32 drops (a constant in two parts, as
+// Cody and Waite's), so the error of h does not grow with g.  In units of
+// 2^-24: ex2 is within 2 ulp (4) and its correction rounds once, which counts
+// r = 1 / (1 + t) times in t r; 1 + t rounds to r, rcp is within 1 ulp (1 / r,
+// as 1/2 <= r <= 1) and three products one rounding each: 6 r + 1 / r + 3 <= 10
+// units of |silu(g) u|, and half a step of t and of g t where these are
+// subnormal (g < -87.3).  At |g| = 106 t is 0.
 __device__ __forceinline__ float gate(float g, float u) {
   constexpr double kLog2e64 = 1.4426950408889634, kLn2 = 0.6931471805599453;  // log2 e, ln 2
   constexpr float kLog2e = static_cast<float>(kLog2e64), kLog2eRest = static_cast<float>(kLog2e64 - kLog2e);
-  const float c = fminf(fmaxf(g, -88.0f), 88.0f);  // keeps 2^h finite; a NaN comes back in the last line
+  const float c = fminf(fabsf(g), 106.0f);  // a NaN comes back in the last line
   const float h = c * -kLog2e;
   const float l = fmaf(c, -kLog2eRest, fmaf(c, -kLog2e, -h));
   float p, r;
   asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(h));
   const float t = fmaf(p, l * static_cast<float>(kLn2), p);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
-  return g * r * u;
+  return (g < 0.0f ? g * t : g) * r * u;
 }
 
 // The int32 -> binary32 conversion, rounded once, without the conversion unit:

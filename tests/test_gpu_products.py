@@ -247,6 +247,26 @@ def test_gate_over_its_whole_range(L):
     assert (Y[d.isfinite() & (y > 3.41e38)] == float("inf")).all()
 
 
+@pytest.mark.parametrize("u", [1.0, 2.0 ** 100, -3e38])
+def test_gate_where_its_reciprocal_is_subnormal(L, u):
+    """silu(g) u for g from -110 to -80, where 1 / (1 + e^-g) leaves binary32's normal range at -87.34 but silu(g) u
+    need not: 10 u of the value, and a step of e^g where that is subnormal (2^-149, for its own rounding and the
+    correction's, half a step each), times |g u|, half a step of g e^g (2^-150 |u|) and of the output."""
+    g = torch.cat([torch.linspace(-110, -80, 30001), torch.linspace(-88, -87, 5001)]).float().cuda()
+    Xq = torch.zeros(g.numel(), 16, dtype=torch.int8, device="cuda")
+    Xq[:, 0] = 1
+    Wq = torch.zeros(32, 16, dtype=torch.int8, device="cuda")
+    Wq[:16, 0], one = 1, torch.ones(32, device="cuda")
+    b = torch.cat([torch.zeros(16), torch.full((16,), u)]).cuda()
+    Y = L.llmint8_scaled_matmul(Xq, g, Wq, one, bias=b, gated=True, dtype=torch.float32)
+    d, v = g.double(), float(b[-1])
+    y = (v * d * torch.sigmoid(d))[:, None].expand(-1, 16)
+    tol = 10 * U * y.abs() + ((d.abs() * 2.0 ** -149 + 2.0 ** -150) * abs(v))[:, None] * (1 + 2.0 ** -20) + 2.0 ** -150
+    check(Y, y, tol)
+    if abs(v) > 1:
+        assert (Y[(d > -95)] != 0).all()
+
+
 # ------------------------------------------------------------------ grouped product
 
 GROUPS = [([1], 64, 128), ([3, 0, 5], 100, 144), ([0, 0, 7, 0], 40, 16), ([16, 17, 15, 1, 0, 33], 257, 272),
