@@ -300,6 +300,88 @@ def test_grouped_matmul(L, sizes, N, K, gated, dtype):
                                           dtype), f"group {e}")
 
 
+# ------------------------------------------------------------------ weights beyond L2, tiles of two halves in a row
+
+def plan(L, S, N, K, E=None, gated=False):
+    """(halves of a tile, tiles, weights leave L2 first) as the call on this device plans them."""
+    import ctypes
+    props = torch.cuda.get_device_properties(0)
+    out = (ctypes.c_int64 * 10)()
+    assert L.load_library().llmint8_product_plan_debug(S, N, K, E or 1, int(E is not None), int(gated),
+                                                       props.multi_processor_count // 2, props.L2_cache_size, out) == 0
+    return out[3], out[8], out[9]
+
+
+def just_beyond_l2(K, E=1):
+    """The fewest channels, a multiple of 32 and some, with which the weights are more than L2 holds."""
+    return (torch.cuda.get_device_properties(0).L2_cache_size // (E * K) // 32 + 1) * 32
+
+
+@pytest.mark.parametrize("T,K,gated,halves", [(1, 4096, False, 1), (16, 4080, True, 1), (150, 4096, True, 1),
+                                              (256, 2736, False, 1), (270, 4096, False, 2), (270, 4080, True, 2),
+                                              (300, 8192, False, 2), (600, 4096, False, 1)])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_scaled_matmul_with_weights_beyond_l2(L, T, K, gated, halves, dtype):
+    """Weights that one tile alone reads leave L2 first; calls one after the other, and where several tiles share them."""
+    N = just_beyond_l2(K) + (0 if gated else 9)
+    planned, _, first_out = plan(L, T, N, K, gated=gated)
+    assert planned == halves and first_out == 1
+    g = gen(T + N)
+    Xq, Wq = codes(g, T, K), codes(g, N, K)
+    sx, sw = scales(g, 0.02, T), scales(g, 0.02 / K ** 0.5, N)
+    b = torch.randn(N, generator=g, device="cuda")
+    y, tol = expected(Xq, sx, Wq, sw, b, gated, dtype)
+    for _ in range(2):
+        Y = torch.empty(T, N // 2 if gated else N, dtype=dtype, device="cuda")
+        L.llmint8_scaled_matmul(Xq, sx, Wq, sw, bias=b, gated=gated, Y=Y)
+        check(Y, y, tol)
+
+
+@pytest.mark.parametrize("K", [2048, 2032])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_grouped_matmul_with_weights_beyond_l2(L, K, gated, dtype):
+    """Groups of one tile, whose weights leave L2 first, beside groups of several and empty ones; rows before and
+    behind them."""
+    sizes = [0, 1, 20, 700, 0, 33, 260, 5, 64, 0, 0, 513, 16, 17, 1, 0]
+    E, lead, tail = len(sizes), 2, 7
+    N = just_beyond_l2(K, E)
+    bounds = lead + np.concatenate([[0], np.cumsum(sizes)])
+    S = int(bounds[-1]) + tail
+    assert plan(L, S, N, K, E, gated)[2] == 1
+    g = gen(K + gated)
+    Xq, Wq = codes(g, S, K), codes(g, E, N, K)
+    sx, sw = scales(g, 0.02, S), scales(g, 0.02 / K ** 0.5, E, N)
+    b = torch.randn(E, N, generator=g, device="cuda")
+    offsets = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    Y = torch.full((S, N // 2 if gated else N), 555.0, dtype=dtype, device="cuda")
+    L.llmint8_grouped_matmul(Xq, sx, offsets, Wq, sw, bias=b, gated=gated, Y=Y)
+    assert (Y[:lead] == 555).all() and (Y[S - tail:] == 555).all()
+    for e in range(E):
+        lo, hi = bounds[e], bounds[e + 1]
+        if hi > lo:
+            check(Y[lo:hi], *expected(Xq[lo:hi], sx[lo:hi], Wq[e], sw[e], b[e], gated, dtype), f"group {e}")
+
+
+@pytest.mark.parametrize("T,N,K,gated", [(1051, 12297, 8064, False), (1051, 12288, 8064, True),
+                                         (1500, 18944, 8192, False), (1500, 18944, 8192, True),
+                                         (1051, 12297, 8080, False)])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_tiles_of_two_halves_one_after_the_other(L, T, N, K, gated, dtype):
+    """Two and three such tiles a pair: the products wait for both accumulators, and the ring goes on from tile to
+    tile."""
+    halves, tiles, _ = plan(L, T, N, K, gated=gated)
+    assert halves == 2 and tiles > 1.9 * (torch.cuda.get_device_properties(0).multi_processor_count // 2)
+    g = gen(T + N)
+    Xq, Wq = codes(g, T, K), codes(g, N, K)
+    sx, sw = scales(g, 0.02, T), scales(g, 0.02 / K ** 0.5, N)
+    b = torch.randn(N, generator=g, device="cuda")
+    Y, untouched = fenced(T, N // 2 if gated else N, dtype)
+    L.llmint8_scaled_matmul(Xq, sx, Wq, sw, b, gated=gated, Y=Y)
+    check(Y, *expected(Xq, sx, Wq, sw, b, gated, dtype))
+    untouched()
+
+
 def test_grouped_matmul_of_one_group_is_the_dense_product(L):
     g = gen(3)
     Xq, Wq = codes(g, 77, 256), codes(g, 320, 256)
