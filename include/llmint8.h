@@ -337,9 +337,10 @@ typedef enum { LLMINT8_F16 = 0, LLMINT8_BF16 = 1, LLMINT8_F32 = 2 } llmint8_dtyp
  *   positions int32 [T][copies]: row t goes to every row positions[t][j] >= 0
  *     of Xq [S][K], xscale [S] (a mixture of experts' order, as
  *     llmint8_expert_positions gives it); -1 is skipped, rows that no position
- *     names are left as they were.  Positions must be distinct: which of two
- *     rows with one position stays is not defined.  A position below -1 or
- *     from S on is skipped and recorded; llmint8_sync_status then reports
+ *     names are left as they were.  Positions must be distinct: a row that two
+ *     tokens name is written by both at once, and its codes and its scale may
+ *     then be partly one's and partly the other's (no other row is touched).
+ *     A position below -1 or from S on is skipped and recorded; llmint8_sync_status then reports
  *     LLMINT8_ERR_INVALID_ARG.
  */
 LLMINT8_API int llmint8_quantize_rows(const void* X, int dtype, int64_t T, int64_t K, const int32_t* positions,

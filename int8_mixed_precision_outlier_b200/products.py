@@ -87,7 +87,8 @@ def llmint8_quantize_rows(X: torch.Tensor, positions: torch.Tensor | None = None
     With positions (int32 [T, k], llmint8_expert_positions) row t is written to
     every row positions[t, j] >= 0 of Xq [S, K] and xscale [S]; S is T k unless
     Xq is given, and rows that no position names are left as they were.
-    Positions must be distinct.  A row with a NaN or an infinity gets the scale
+    Positions must be distinct: what a row that is named twice holds is not
+    defined, not even that its codes and scale are of one token.  A row with a NaN or an infinity gets the scale
     NaN and codes 0."""
     try:
         T, K = X.shape
