@@ -769,10 +769,12 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
     const int H = product::BM, nN = static_cast<int>((static_cast<int64_t>(N) + 2 * H - 1) / (2 * H));
     const int64_t wide = (avg + 2 * product::MAX_BT - 1) / (2 * product::MAX_BT);
     const int half = columns((avg + 2 * wide - 1) / (2 * wide));
-    const double rounds = std::ceil(static_cast<double>(wide) * nN / max_pairs);
-    const double cost = rounds * (KB * (0.04 + 0.00104 * 2 * half + 0.0004 * H) + 0.5 + 0.006 * 2 * half) +
-                        0.7 * std::min(static_cast<double>(wide) * nN / max_pairs, 1.0);
-    if (cost < 0.95 * best_cost && (2 * wide - 1) * half < avg) {  // every half has rows
+    const int64_t last = avg - (2 * wide - 1) * half;  // rows of the last half
+    const double tiles = static_cast<double>(wide) * nN / max_pairs;
+    const double cols = static_cast<double>((2 * wide - 1) * half + columns(last)) / static_cast<double>(wide);
+    const double cost = std::ceil(tiles) * (KB * (0.04 + 0.00104 * cols + 0.0004 * H) + 0.5 + 0.006 * cols) +
+                        0.7 * std::min(tiles, 1.0);
+    if (cost < 0.95 * best_cost && last > 0) {  // every half has rows
       best.wide = true;
       best.H = H;
       best.BT = half;

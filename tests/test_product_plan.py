@@ -139,9 +139,11 @@ def test_which_plans_the_tested_shapes_take(lib):
     GPU: a change of the plan's constants may not take one of them away unseen."""
     halves = {s: plan(lib, *s[:3], gated=s[3]).halves for s in
               [(257, 13824, 2048, False), (270, 18944, 2064, True), (600, 9001, 4096, False),
-               (513, 8192, 4112, True), (1051, 12297, 8064, False), (150, 40000, 128, False)]}
+               (513, 8192, 4112, True), (1051, 12297, 8064, False), (1213, 18442, 6160, False),
+               (150, 40000, 128, False)]}
     assert halves[257, 13824, 2048, False] == 2 and halves[270, 18944, 2064, True] == 2
-    assert halves[1051, 12297, 8064, False] == 2 and halves[150, 40000, 128, False] == 1
+    assert halves[1051, 12297, 8064, False] == 2 and halves[1213, 18442, 6160, False] == 2
+    assert halves[150, 40000, 128, False] == 1
     assert plan(lib, 64, 4096, 512).KPB == 2 and plan(lib, 16, 4096, 4096).KPB == 4 and plan(lib, 33, 257, 272).KPB == 1
     assert plan(lib, 16, 4096, 2048, E=16).drop == 1 and plan(lib, 16, 4096, 2048, E=8).drop == 0
 
