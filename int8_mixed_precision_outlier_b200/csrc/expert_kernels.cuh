@@ -117,8 +117,11 @@ __device__ __forceinline__ void code_chunk(const Chunk& k, float s, float inv, u
 // codes; VPT = 0: read again (from L1 or L2).  Without positions row t goes to
 // row t; with them, to every row positions[t * copies + j] >= 0.
 //
-// Bound by memory: 4096 x 8192 fp16 takes 22.5 us (4.5 TB/s, the codes staying
-// in L2); 40 registers keep 1536 threads on an SM (with 72 it took 33 us).
+// Bound by memory where there are many bytes: 8192 x 4096 binary32 takes 25.6 us
+// (6.6 TB/s, the copy rate), 4096 x 8192 fp16 18.9 (5.3 TB/s), 2048 x 4096 fp16
+// 7.4 (3.4 TB/s; 5.3 us with the rows in L2), where a row's load, maximum and
+// stores, one after the other, count.  40 registers let 1536 threads on an SM;
+// a limit of 72 measured the same.
 template <int IT, int VPT>
 __global__ void __maxnreg__(40)
     quantize_rows_kernel(const void* X, int K, const int32_t* positions, int copies, int S, int8_t* Xq,
@@ -207,9 +210,10 @@ __global__ void __maxnreg__(40)
 // atomics: the result does not depend on timing.
 //
 // Bound by latency: the ids are loaded once, all in flight, and stay in
-// registers with their ranks (65536 choices of 128 experts: 11.4 us, 19.7 with
-// a second pass over the ids).  ITEMS > 0: at most ITEMS ids a lane.  ITEMS = 0:
-// any number; the ranks wait in `positions` and the ids are read again.
+// registers with their ranks (65536 choices of 128 experts: 8.45 us, 8.53 with a
+// second pass over the ids; 320000 of 256, which takes it, 28.5).  ITEMS > 0: at
+// most ITEMS ids a lane.  ITEMS = 0: any number; the ranks wait in `positions`
+// and the ids are read again.
 constexpr int kPosThreads = 1024;
 constexpr int kPosWarps = kPosThreads / 32;
 constexpr int kPosMaxCtas = 16;  // a cluster size that a kernel has to opt in to
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kPosThreads, 1)
   auto key_of = [&](ID v) { return v >= 0 && v < static_cast<ID>(E) ? static_cast<int>(v) : -1; };
   int* mine = cnt + warp * E;
   // The lanes with this lane's key, by one ballot per bit (match.any compares
-  // lane by lane: with it 65536 choices of 128 experts took 17.5 us).
+  // lane by lane: with it 65536 choices of 128 experts take 10.2 us).
   const int bits = 32 - __clz(E);  // of keys in [0, E), and E for none
   auto alike = [&](int key) {
     const uint32_t k = static_cast<uint32_t>(key >= 0 ? key : E);
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(kPosThreads, 1)
 // over the j with a position, in binary32 and ascending j (one order, so the
 // result does not depend on timing), rounded once.  Y's rows are read once
 // and 16 bytes at a time where N and the types allow.  Bound by memory: 4096
-// tokens of 4 rows of 5120, bf16, take 36.5 us (5.7 TB/s).
+// tokens of 4 rows of 5120, bf16, take 36.0 us (5.8 TB/s).
 constexpr int kCombineThreads = 128;
 
 template <int T>

@@ -726,8 +726,8 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   // 64 columns) + 0.4 ns a weight row of the CTA (the copies; below 64 rows they
   // cost no less), the last tile's outputs at 6 ns a column, and a wave
   // that is cut finer reads more operands (0.7 us for a full one):
-  // 333 x 13824 x 5120 takes 24.4 us with 2 rounds of 176 x 192, 29.3 with 176
-  // x 256, 27.5 with 3 rounds of 96 x 256.
+  // 333 x 13824 x 5120 takes 26.6 us with 2 rounds of 192 x 192, 27.6 with 192
+  // x 256, 29.1 with 3 rounds of 96 x 256 (tiles of one accumulator each).
   double best_cost = -1.0;
   auto consider = [&](int H, int nN, int BT, int64_t mt) {
     const double tiles = static_cast<double>(groups) * static_cast<double>(mt) * nN / max_pairs;
@@ -761,10 +761,10 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   // Tiles of two halves of up to 256 tokens each, which share the copies of the
   // weights and take both accumulators.  Nothing overlaps their outputs, so
   // they pay where they save a round or narrow tiles: 333 x 13824 x 5120 takes
-  // 24.1 us with them and 25.6 without (27.8 and 30.7 at the sustained clock),
-  // 257 x 13824 x 5120 20.4 and 23.1, 1024 x 8192 x 8192 48.5 and 53.4; where
-  // the estimate says no, 512 x 27648 x 5120 61.9 and 52.8, 4096 x 28672 x 8192
-  // 685 and 651.
+  // 25.3 us with them and 26.6 without (27.5 and 31.2 at the sustained clock),
+  // 257 x 13824 x 5120 22.2 and 24.4, 1024 x 8192 x 8192 48.0 and 51.2; where
+  // the estimate says no, 512 x 27648 x 5120 60.9 and 54.0, 4096 x 28672 x 8192
+  // 610 and 584.
   if (!grouped && avg > product::MAX_BT) {
     const int H = product::BM, nN = static_cast<int>((static_cast<int64_t>(N) + 2 * H - 1) / (2 * H));
     const int64_t wide = (avg + 2 * product::MAX_BT - 1) / (2 * product::MAX_BT);
@@ -788,7 +788,7 @@ ProductPlan plan_product(int S, int N, int K, int E, bool grouped, bool gated, i
   // k-blocks per stage: a stage costs the issuing warps about 300 cycles and
   // its products 2 a token column and k-block (160 at least), so stages of
   // narrow tiles hold more; four stages at least, or the loads wait.
-  // 16 x 4096 x 4096: 11.1, 8.2, 7.3 us with 1, 2, 4 k-blocks.
+  // 16 x 4096 x 4096: 11.2, 7.6, 6.4 us with 1, 2, 4 k-blocks.
   const int cols = std::min(best.BT << best.wide, columns(avg));
   const int wish = cols >= 224 ? 1 : cols >= 96 ? 2 : product::KPB_MAX;
   const int kblock = (best.H + (best.b_rows << best.wide)) * product::BK;
@@ -875,7 +875,8 @@ int product_impl(const int8_t* Xq, const float* sx, int64_t S, int64_t K, const 
   for (int i = 0; i < 4; ++i)
     if (i < least || i * p.quarter >= p.b_rows) tx.m[i] = tx.m[least];
   if (!ok) return LLMINT8_ERR_CUDA;
-  const ProductKernel kern = gated ? product_kernel_for<true>(dtype, plan.wide) : product_kernel_for<false>(dtype, plan.wide);
+  const ProductKernel kern =
+      gated ? product_kernel_for<true>(dtype, plan.wide) : product_kernel_for<false>(dtype, plan.wide);
   const int pairs = static_cast<int>(std::min<int64_t>(max_pairs, plan.tiles));
   const cudaError_t e = launch_ex(kern, dim3(2 * pairs), dim3(product::THREADS), product::SMEM_BYTES,
                                   static_cast<cudaStream_t>(stream), true, 2, tw, tx, p);

@@ -26,10 +26,10 @@
 // 256-column accumulators let the next tile's products run while the epilogue
 // drains the last one.  Every mbarrier wait is bounded.
 //
-// Few tokens are bound by reading the weights (1 x 11008 x 4096: 10.6 us, 45 MB
-// at 4.2 TB/s with the launch and the last tiles in it), many by the tensor
-// cores and the copies of the operands from L2 (4096 x 28672 x 8192: 567 us,
-// 3.4 POP/s; 661 us sustained, at the card's 1000 W).
+// Few tokens are bound by reading the weights (1 x 11008 x 4096: 10.9 us, 45 MB
+// at 4.1 TB/s with the launch and the last tiles in it), many by the tensor
+// cores (4096 x 28672 x 8192: 583 us, 3.3 POP/s; 654 us sustained, at the card's
+// 1000 W).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -386,9 +386,9 @@ struct Epilogue {
 // M = 256): CTA r holds weight rows H r .. of the tile and half of its tokens
 // as operands, and after the products H rows by all tokens in its TMEM.  The
 // even CTA's elected thread issues the MMAs; both CTAs' copies complete on its
-// `full` barriers, and each commit arrives at both CTAs.  (Single CTAs with
-// tiles of 128 rows were within 3 % of pairs on the smallest shapes, up to
-// 27 % behind on others.)
+// `full` barriers, and a stage's or a tile's commit arrives at both CTAs.
+// (Single CTAs with tiles of 128 rows were within 3 % of pairs on the smallest
+// shapes, up to 27 % behind on others.)
 //
 // WIDE tiles have two halves of up to MAX_BT tokens, one accumulator
 // each: a stage brings the weights once and the token rows of both, and the
@@ -525,10 +525,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool issuer = elect_one();
     // Weights that no other tile reads, of a call whose weights are more than L2
     // holds (none would be there at the next call), leave L2 first: 256 tokens
-    // to 4 of 32 experts of 4096 x 2048 take 44.3 us, 47.7 without; 500 to 2 of 8
-    // of 8192 x 4096 48.6 and 51.6; 150 x 27648 x 5120 28.8 and 29.9.  (Where a
-    // group has several tiles it costs 1 to 3 %, for smaller weights that would
-    // have stayed, 64 x 4096 x 4096, 1.2 us of 6.6.)
+    // to 4 of 32 experts of 4096 x 2048 take 45.0 us, 47.0 without; 500 to 2 of 8
+    // of 8192 x 4096 51.4 and 53.4; 150 x 27648 x 5120 29.6 and 30.4.  (Smaller
+    // weights that would have stayed: 16 x 4096 x 4096 6.35 with it and without,
+    // 6.47 and 6.36 sustained, 32 x 8192 x 4096 8.94 and 8.88.)
     const uint64_t first_out = policy_evict_first();
     previous_done();
     int s = 0;              // the stage to fill next
